@@ -19,11 +19,17 @@ Names follow the C ABI:
 * :func:`spec_draft_step` -- one draft step through the target's LM head
   (``include/spec_draft.h``);
 * :func:`spec_tree_verify` / :func:`spec_tree_verify_from_logits` -- tree-shaped
-  candidates (``include/spec_tree.h``).
+  candidates (``include/spec_tree.h``);
+* :func:`spec_kv_attention` / :func:`spec_prompt_attention` -- attention of new
+  tokens over the paged cache and of packed prompts (``include/spec_attention.h``);
+* :func:`spec_kv_release` / :func:`spec_kv_fork` / :func:`spec_kv_reserve` /
+  :func:`spec_kv_compact` -- the cache's pages, and :func:`spec_kv_commit_path`
+  -- commit of an accepted tree path (``include/spec_kv_pages.h``).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -36,6 +42,10 @@ __all__ = [
     "ngram_workspace", "spec_ngram_propose", "ngram_read_error",
     "draft_step_workspace_bytes", "spec_draft_step",
     "tree_workspace_bytes", "spec_tree_verify", "spec_tree_verify_from_logits",
+    "kv_attention_workspace", "spec_kv_attention", "prompt_attention_workspace", "spec_prompt_attention",
+    "attention_read_error",
+    "kv_pages_workspace", "spec_kv_release", "spec_kv_fork", "spec_kv_reserve", "spec_kv_compact",
+    "kv_path_workspace", "spec_kv_commit_path", "kv_pages_read_error",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspec_verify.so")
@@ -60,6 +70,20 @@ class SpecNgramDims(ctypes.Structure):
 
 class SpecTreeDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("V", ctypes.c_int32)]
+
+
+class SpecKvAttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "S", "heads", "kv_heads", "head_dim", "page_size", "num_pages",
+                                              "max_pages", "dtype")] + [("q_stride", ctypes.c_int64)]
+
+
+class SpecPromptDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "heads", "kv_heads", "head_dim", "total_q", "total_k", "dtype")] \
+        + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class SpecKvPagesDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "max_pages", "num_pages", "page_size")]
 
 
 class SpecError(RuntimeError):
@@ -100,6 +124,21 @@ _SIGS = {
     "spec_draft_step": (ctypes.c_int, [_VP, _VP, _VP, _F32, _VP, _VP, ctypes.c_int64, SpecDims, _VP, _SZ, _VP]),
     "spec_ngram_propose": (ctypes.c_int, [_VP, _VP, _VP, _VP, SpecNgramDims, _VP, _SZ, _VP]),
     "spec_ngram_read_error": (ctypes.c_int, [_VP, ctypes.POINTER(_I32), _VP]),
+    "spec_kv_attention_workspace_bytes": (_SZ, [SpecKvAttnDims]),
+    "spec_prompt_attention_workspace_bytes": (_SZ, [SpecPromptDims]),
+    "spec_kv_attention": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _F32, _VP, _VP, SpecKvAttnDims, _VP, _SZ,
+                                         _VP]),
+    "spec_prompt_attention": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _F32, _VP, _VP, SpecPromptDims, _VP, _SZ, _VP]),
+    "spec_attention_read_error": (ctypes.c_int, [_VP, ctypes.POINTER(_I32), _VP]),
+    "spec_kv_pages_workspace_bytes": (_SZ, [SpecKvPagesDims]),
+    "spec_kv_release": (ctypes.c_int, [_VP, _VP, _VP, _VP, SpecKvPagesDims, _VP, _SZ, _VP]),
+    "spec_kv_fork": (ctypes.c_int, [_VP, _VP, _I32, _VP, _VP, _VP, SpecKvPagesDims, _VP, _SZ, _VP]),
+    "spec_kv_reserve": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _I32, ctypes.c_int64, SpecKvPagesDims, _VP, _SZ,
+                                       _VP]),
+    "spec_kv_compact": (ctypes.c_int, [_VP, _VP, _VP, _I32, ctypes.c_int64, _VP, SpecKvPagesDims, _VP, _SZ, _VP]),
+    "spec_kv_pages_read_error": (ctypes.c_int, [_VP, ctypes.POINTER(_I32), _VP]),
+    "spec_kv_path_workspace_bytes": (_SZ, [SpecKvDims]),
+    "spec_kv_commit_path": (ctypes.c_int, [_VP, _VP, _VP, _VP, _VP, _VP, SpecKvDims, _VP, _SZ, _VP]),
 }
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -577,3 +616,356 @@ def spec_tree_verify_from_logits(target_logits, draft_logits, tokens, parents, u
         _ptr(uniforms if T > 0 else None), T, _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), SpecTreeDims(B, N, 0, V),
         _ptr(workspace), workspace.numel(), _stream(stream)))
     return outs
+
+
+# ------------------------------------------------- cache operators: common
+def _one_device(first, name, *others):
+    """The device of ``first``; every other given tensor must lie on it."""
+    if not first.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must lie on {dev}, got one on {t.device}")
+    return dev
+
+
+class _Launch:
+    """Makes ``stream`` (default: the current stream of ``device``) and its
+    device current for the call, so that what is allocated in it belongs to
+    the stream the kernels run on."""
+    __slots__ = ("stream", "context")
+
+    def __init__(self, device, stream):
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+            self.context = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        else:
+            if stream.device != device:
+                raise ValueError(f"the stream belongs to {stream.device}, the tensors lie on {device}")
+            self.stream = stream
+            self.context = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+
+
+def _int32(t, name, shape):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, nbytes, device):
+    """The caller's workspace, checked, or a zeroed one of ``nbytes``."""
+    if nbytes == 0:
+        raise ValueError("invalid sizes")
+    if workspace is None:
+        return torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _read_word(fn, workspace, stream):
+    word = ctypes.c_int32(0)
+    with _Launch(workspace.device, stream) as s:
+        _check(fn(workspace.data_ptr(), ctypes.byref(word), s))
+    return int(word.value)
+
+
+# ---------------------------------------------------------------- attention
+ATTN_DEVERR_CAPACITY, ATTN_DEVERR_PAGE, ATTN_DEVERR_LENGTH, ATTN_DEVERR_TREE, ATTN_DEVERR_TIMEOUT = 1, 2, 4, 8, 16
+_ATTN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _attn_dtype(q, *others):
+    code = _ATTN_DTYPES.get(q.dtype)
+    if code is None:
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    for t in others:
+        if t is not None and t.dtype != q.dtype:
+            raise ValueError(f"all of q, keys, values and out must share a dtype, got {q.dtype} and {t.dtype}")
+    return code
+
+
+def _token_stride(t, name):
+    """Elements from one token to the next of [tokens][heads][head_dim], heads dense."""
+    heads, D = t.shape[-2:]
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    if t.shape[-3] == 1:
+        return heads * D if t.dim() == 3 or t.shape[0] == 1 else t.stride(0)
+    stride = t.stride(-3)
+    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * stride:
+        raise ValueError(f"the tokens of {name} must be evenly spaced")
+    return stride
+
+
+def _kv_attn_dims(q, pool, max_pages):
+    if q.dim() != 4:
+        raise ValueError("q must be [B][S][heads][head_dim]")
+    if pool.dim() != 3 or not pool.is_contiguous():
+        raise ValueError("pool must be one layer's contiguous plane [num_pages][page_size][entry]")
+    B, S, heads, D = q.shape
+    kv_heads, rest = divmod(pool.shape[2], 2 * D)
+    if rest:
+        raise ValueError(f"an entry of {pool.shape[2]} elements is not [2][kv_heads][{D}]")
+    return SpecKvAttnDims(B, S, heads, kv_heads, D, pool.shape[1], pool.shape[0], max_pages, _attn_dtype(q, pool),
+                          _token_stride(q, "q"))
+
+
+def kv_attention_workspace(q, pool) -> torch.Tensor:
+    """A zeroed workspace for :func:`spec_kv_attention` calls shaped like ``q``
+    and ``pool`` (reusable; each call leaves it ready for the next)."""
+    dims = _kv_attn_dims(q, pool, 1)
+    return _scratch(None, library().spec_kv_attention_workspace_bytes(dims), _one_device(q, "q", pool))
+
+
+def spec_kv_attention(q, pool, block_table, seq_len, staged=None, *, parents=None, q_len=None, scale=None, out=None,
+                      out_lse=None, workspace=None, stream=None):
+    """Attention of the newest tokens over the paged cache.
+
+    ``q`` [B, S, heads, head_dim] bf16 or fp16 (tokens may be strided, e.g. a
+    slice of a fused projection), ``pool`` one layer's plane [num_pages,
+    page_size, 2*kv_heads*head_dim], ``block_table`` int32 [B, max_pages],
+    ``seq_len`` int32 [B] committed positions, ``staged`` [B, S, entry] the new
+    tokens' entries or None (they are in the pool behind the committed ones).
+    ``parents`` int32 [B, S] makes the new tokens a tree (None: a chain),
+    ``q_len`` int32 [B] limits the rows of a sequence.  ``scale`` defaults to
+    head_dim ** -0.5.  Returns ``out`` like q; ``out_lse`` f32 [B, S, heads]
+    receives the log-sum-exp where given."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_pages]")
+    dims = _kv_attn_dims(q, pool, block_table.shape[1])
+    B, S = q.shape[:2]
+    dev = _one_device(q, "q", pool, block_table, seq_len, staged, parents, q_len, out, out_lse, workspace)
+    _attn_dtype(q, staged, out)
+    _int32(block_table, "block_table", (B, dims.max_pages))
+    _int32(seq_len, "seq_len", (B,))
+    if staged is not None and (staged.shape != (B, S, pool.shape[2]) or not staged.is_contiguous()):
+        raise ValueError(f"staged must be contiguous [{B}][{S}][{pool.shape[2]}], got {tuple(staged.shape)}")
+    if parents is not None:
+        _int32(parents, "parents", (B, S))
+    if q_len is not None:
+        _int32(q_len, "q_len", (B,))
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous {tuple(q.shape)}")
+    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != q.shape[:3]
+                                or not out_lse.is_contiguous()):
+        raise ValueError(f"out_lse must be contiguous float32 {tuple(q.shape[:3])}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(dims.head_dim)
+    lib = library()
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        workspace = _scratch(workspace, lib.spec_kv_attention_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_attention(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seq_len.data_ptr(),
+                                     _at(staged), _at(parents), _at(q_len), scale, out.data_ptr(), _at(out_lse), dims,
+                                     workspace.data_ptr(), workspace.numel(), s))
+    return out
+
+
+def _prompt_dims(q, k, v, B):
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [total_q][heads][head_dim], k and v [total_k][kv_heads][head_dim]")
+    return SpecPromptDims(B, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], _attn_dtype(q, k, v),
+                          _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
+
+
+def prompt_attention_workspace(q, k, B: int) -> torch.Tensor:
+    """A zeroed workspace for :func:`spec_prompt_attention` calls on ``B``
+    sequences shaped like ``q`` and ``k`` (reusable)."""
+    dims = _prompt_dims(q, k, k, B)
+    return _scratch(None, library().spec_prompt_attention_workspace_bytes(dims), _one_device(q, "q", k))
+
+
+def spec_prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=None, workspace=None,
+                          stream=None):
+    """Causal attention over packed sequences: ``q`` [total_q, heads,
+    head_dim], ``k`` and ``v`` [total_k, kv_heads, head_dim] bf16 or fp16
+    (tokens may be strided), ``cu_q`` / ``cu_k`` int32 [B + 1] offsets (``cu_k``
+    None: the same).  A sequence with more keys than queries holds the last
+    part of a prompt.  Returns ``out`` like q (rows that belong to no sequence
+    are left as they were; zeros when ``out`` is made here)."""
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must be [B + 1]")
+    B = cu_q.shape[0] - 1
+    dims = _prompt_dims(q, k, v, B)
+    dev = _one_device(q, "q", k, v, cu_q, cu_k, out, out_lse, workspace)
+    _attn_dtype(q, out)
+    _int32(cu_q, "cu_q", (B + 1,))
+    if cu_k is not None:
+        _int32(cu_k, "cu_k", (B + 1,))
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous {tuple(q.shape)}")
+    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != q.shape[:2]
+                                or not out_lse.is_contiguous()):
+        raise ValueError(f"out_lse must be contiguous float32 {tuple(q.shape[:2])}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(dims.head_dim)
+    lib = library()
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.zeros(q.shape, dtype=q.dtype, device=dev)
+        workspace = _scratch(workspace, lib.spec_prompt_attention_workspace_bytes(dims), dev)
+        _check(lib.spec_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _at(cu_k), scale,
+                                         out.data_ptr(), _at(out_lse), dims, workspace.data_ptr(), workspace.numel(),
+                                         s))
+    return out
+
+
+def attention_read_error(workspace, stream=None) -> int:
+    """Synchronises the stream; the error word (ATTN_DEVERR_* bits) of the
+    latest attention call on ``workspace``."""
+    return _read_word(library().spec_attention_read_error, workspace, stream)
+
+
+# -------------------------------------------------------------- cache pages
+KV_DEVERR_PATH, KV_DEVERR_REF, KV_DEVERR_PAIR, KV_DEVERR_BUSY, KV_DEVERR_POOL = 8, 16, 32, 64, 128
+
+
+def _pages(block_table, ref_count, page_size, seq_len, *others):
+    if block_table.dim() != 2 or ref_count.dim() != 1:
+        raise ValueError("block_table must be [B][max_pages] and ref_count [num_pages]")
+    dev = _one_device(block_table, "block_table", ref_count, seq_len, *others)
+    dims = SpecKvPagesDims(block_table.shape[0], block_table.shape[1], ref_count.shape[0], page_size)
+    _int32(block_table, "block_table", (dims.B, dims.max_pages))
+    _int32(ref_count, "ref_count", (dims.num_pages,))
+    if seq_len is not None:
+        _int32(seq_len, "seq_len", (dims.B,))
+    return dev, dims
+
+
+def _pool_planes(pool, num_pages):
+    if pool.dim() != 4 or not pool.is_contiguous() or pool.shape[1] != num_pages:
+        raise ValueError("pool must be contiguous [layers][num_pages][page_size][E] with ref_count's pages")
+    return pool.shape[0], pool.shape[3] * pool.element_size()
+
+
+def kv_pages_workspace(block_table, ref_count) -> torch.Tensor:
+    """A zeroed workspace for the page operators on this table and pool (reusable)."""
+    dev, dims = _pages(block_table, ref_count, 1, None)
+    return _scratch(None, library().spec_kv_pages_workspace_bytes(dims), dev)
+
+
+def spec_kv_release(new_len, seq_len, block_table, ref_count, page_size: int, *, workspace=None, stream=None):
+    """Give back every page behind ``new_len`` (int32 [B]; negative: leave the
+    sequence alone; None: behind ``seq_len``) and set ``seq_len`` to it.
+    ``block_table`` int32 [B, max_pages] (negative: no page), ``ref_count``
+    int32 [num_pages]; all updated in place.  Returns the workspace (its error
+    word is read by :func:`kv_pages_read_error`)."""
+    dev, dims = _pages(block_table, ref_count, page_size, seq_len, new_len, workspace)
+    if new_len is not None:
+        _int32(new_len, "new_len", (dims.B,))
+    lib = library()
+    with _Launch(dev, stream) as s:
+        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_release(_at(new_len), seq_len.data_ptr(), block_table.data_ptr(), ref_count.data_ptr(), dims,
+                                   workspace.data_ptr(), workspace.numel(), s))
+    return workspace
+
+
+def spec_kv_fork(src, dst, seq_len, block_table, ref_count, page_size: int, *, workspace=None, stream=None):
+    """Sequence ``dst[i]`` (holding no page) becomes a copy of ``src[i]`` that
+    shares its pages; ``src`` and ``dst`` int32 [n].  Returns the workspace."""
+    dev, dims = _pages(block_table, ref_count, page_size, seq_len, src, dst, workspace)
+    if src.dim() != 1:
+        raise ValueError("src and dst must be [n]")
+    _int32(src, "src", src.shape)
+    _int32(dst, "dst", src.shape)
+    lib = library()
+    with _Launch(dev, stream) as s:
+        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_fork(src.data_ptr(), dst.data_ptr(), src.shape[0], seq_len.data_ptr(),
+                                block_table.data_ptr(), ref_count.data_ptr(), dims, workspace.data_ptr(),
+                                workspace.numel(), s))
+    return workspace
+
+
+def spec_kv_reserve(num_new, seq_len, block_table, ref_count, pool, *, workspace=None, stream=None):
+    """Make the ``num_new`` (int32 [B]) positions behind ``seq_len`` writable:
+    new pages where the table holds none, own copies of shared ones.  ``pool``
+    [layers, num_pages, page_size, E].  Returns the workspace."""
+    dev, dims = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, seq_len, num_new, pool,
+                       workspace)
+    layers, entry = _pool_planes(pool, dims.num_pages)
+    _int32(num_new, "num_new", (dims.B,))
+    lib = library()
+    with _Launch(dev, stream) as s:
+        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_reserve(num_new.data_ptr(), seq_len.data_ptr(), block_table.data_ptr(),
+                                   ref_count.data_ptr(), pool.data_ptr(), layers, entry, dims, workspace.data_ptr(),
+                                   workspace.numel(), s))
+    return workspace
+
+
+def spec_kv_compact(block_table, ref_count, pool, *, out_num_live=None, workspace=None, stream=None):
+    """Move the live pages to the front of ``pool`` [layers, num_pages,
+    page_size, E]; ``out_num_live`` int32 [1] receives how many there are.
+    Returns the workspace."""
+    dev, dims = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, None, pool, out_num_live,
+                       workspace)
+    layers, entry = _pool_planes(pool, dims.num_pages)
+    if out_num_live is not None:
+        _int32(out_num_live, "out_num_live", (1,))
+    lib = library()
+    with _Launch(dev, stream) as s:
+        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_compact(block_table.data_ptr(), ref_count.data_ptr(), pool.data_ptr(), layers, entry,
+                                   _at(out_num_live), dims, workspace.data_ptr(), workspace.numel(), s))
+    return workspace
+
+
+def kv_path_workspace(B: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for :func:`spec_kv_commit_path` on ``B`` sequences (reusable)."""
+    n = library().spec_kv_path_workspace_bytes(SpecKvDims(B, 1, 1, 1, 1, 1, 16))
+    return _scratch(None, n, torch.device(device))
+
+
+def spec_kv_commit_path(num_accepted, path, seq_len, block_table, pool, staged=None, *, workspace=None, stream=None):
+    """Commit the accepted path of a tree round (``num_accepted`` int32 [B] and
+    ``path`` int32 [B, N] as :func:`spec_tree_verify` returns them): the root's
+    entry and the path's, from ``staged`` [layers, B, N, E] or, when it is None,
+    from positions ``seq_len`` + node of the pool [layers, num_pages,
+    page_size, E]; ``seq_len`` advances.  Returns the workspace (its error word
+    is read by :func:`kv_pages_read_error`)."""
+    if path.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("path must be [B][N] and block_table [B][max_pages]")
+    if pool.dim() != 4 or not pool.is_contiguous():
+        raise ValueError("pool must be contiguous [layers][num_pages][page_size][E]")
+    B, N = path.shape
+    layers, num_pages, page_size, E = pool.shape
+    dev = _one_device(pool, "pool", num_accepted, path, seq_len, block_table, staged, workspace)
+    _int32(path, "path", (B, N))
+    _int32(num_accepted, "num_accepted", (B,))
+    _int32(seq_len, "seq_len", (B,))
+    _int32(block_table, "block_table", (B, block_table.shape[1]))
+    if staged is not None and (staged.dtype != pool.dtype or staged.shape != (layers, B, N, E)
+                               or not staged.is_contiguous()):
+        raise ValueError(f"staged must be contiguous {pool.dtype} [{layers}][{B}][{N}][{E}]")
+    dims = SpecKvDims(B, N, layers, page_size, num_pages, block_table.shape[1], E * pool.element_size())
+    lib = library()
+    with _Launch(dev, stream) as s:
+        workspace = _scratch(workspace, lib.spec_kv_path_workspace_bytes(dims), dev)
+        _check(lib.spec_kv_commit_path(num_accepted.data_ptr(), path.data_ptr(), seq_len.data_ptr(),
+                                       block_table.data_ptr(), _at(staged), pool.data_ptr(), dims,
+                                       workspace.data_ptr(), workspace.numel(), s))
+    return workspace
+
+
+def kv_pages_read_error(workspace, stream=None) -> int:
+    """Synchronises the stream; the error word (KV_DEVERR_* bits) of the latest
+    page operator or path commit on ``workspace``."""
+    return _read_word(library().spec_kv_pages_read_error, workspace, stream)
