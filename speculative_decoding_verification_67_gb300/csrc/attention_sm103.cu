@@ -1,25 +1,78 @@
 // Attention over the paged cache and over packed prompts.  Declared in
 // include/spec_attention.h.
 //
-// Simple form: one warp per (token, head).  Each lane holds head_dim / 32
-// elements of the query and of the output; the warp walks the visible keys
-// once with the running maximum and sum of the softmax, a dot product and its
-// shuffle sum per key.
+// One kernel for both.  A work item is a tile of query rows of one key-value
+// head: row r of a tile is token r / G, head r % G of the group (G = heads /
+// kv_heads), so a key or value is fetched once for all heads that share it.
+// The item walks its keys in blocks of 128 with the running maximum and sum of
+// the softmax:
+//   S = Q K^T            tcgen05.mma, 128 x 128, operands in shared memory
+//   P = exp2(S c - m c)  softmax warps, S read from and P written to TMEM
+//   O = O + P V          tcgen05.mma, P from TMEM, V from shared memory
+// with c = scale log2(e).  m is raised, and O rescaled, only when a row's new
+// maximum exceeds it by more than 2^8 in weight; until then weights up to 2^8
+// stand in P, which costs no precision and spares reading O back for most
+// blocks.
+//
+// Two softmax warpgroups (one row per thread) work on two score tiles, so the
+// tensor core computes for one while the other is in its exponentials:
+//   * prompts: two row tiles of the item share every K and V block;
+//   * cache: the item has one row tile, the warpgroups take even and odd
+//     blocks, each with a running maximum, sum and O of its own, merged at the
+//     end.  With few rows (one token: G of the 128 rows) the tensor core's
+//     work is padding, but at 1024 clocks a block it stays below the ~2200 that
+//     a block's 64 KB take from HBM, which is what bounds it.
+//
+// One CTA per SM walks an equal share of all items' blocks (plus a constant per
+// item for its start and end).  An item cut between CTAs leaves unnormalised
+// partial rows, which a second, small kernel joins.  Shares are computed from the lengths
+// on the device; the host never sees them.
+//
+// Loads: a warp feeds a ring of 128-position K and V tiles by TMA.  Packed
+// keys are boxes of 128 token rows.  Cache positions are looked up in the block table and
+// fetched by four-row gathers, so pages of any size, in any place, and staged
+// entries make the same tile; positions behind the end are rows outside the
+// tensor and arrive as zeros.
+//
+// Masked values: P is 0 where a row must not see a key, but 0 times an
+// infinite or not-a-number value is not 0.  In blocks that some row may not
+// see to the end, the softmax warps look through the V tile first: rows of V
+// with such values are zeroed in shared memory and added, to the rows that do
+// see them, by plain multiplications.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv_copy.cuh"
+#include "sm103_ptx.cuh"
 #include "spec_attention.h"
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kBlock = 128;          // keys per block, rows per tile
+constexpr int kThreads = 320;        // two softmax warpgroups, an MMA warp, a load warp
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
+constexpr int kItemUnits = 2;        // an item's start and end, in blocks
 constexpr int kMaxTree = 256;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 4;        // CTAs that share the rows of one join
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;        // log2 of the largest weight before O is rescaled
+
+// What a join needs to know of an item that was cut (one record per CTA).
+struct Cut {
+  long long start, total;  // first unit of the item, units in all
+  int active;
+  int b, kvh, tile, n;     // the item and its blocks
+  int first;               // the CTA that holds block 0
+};
 
 struct AttnArgs {
   const void* q;
@@ -32,144 +85,1028 @@ struct AttnArgs {
   const int32_t* parents;
   void* out;
   float* lse;
-  float scale;
-  int B, S, heads, kv_heads, page_size, num_pages, max_pages, total_q, total_k;
-  long long q_stride, k_stride, v_stride;
+  float scale_log2;
+  int B, S, heads, kv_heads, G, page_size, num_pages, max_pages, total_q, total_k;
+  int tile_tokens;        // whole tokens in a row tile
+  long long k_stride, v_stride;
+  // workspace
   int* ctrl;
+  int* bad;               // [B] error bits of each sequence (cache)
+  Cut* cuts;              // [kMaxGrid]
+  float* part_o;          // [kMaxGrid][2][rows][D]
+  float2* part_ml;        // [kMaxGrid][2][rows] (reference in log2, sum)
 };
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(__half& y, float x) { y = __float2half_rn(x); }
-
-// One sequence as the kernel sees it.
+// One sequence: Lq queries behind `base` keys (packed: negative when there are fewer keys than queries).
 struct Seq {
-  int Lq, Lk;           // queries, keys (new ones included)
-  int q0;               // first row of q
-  long long k0;         // first row of packed keys
-  int err;
+  int Lq, base, q0, tiles;
+  long long k0;
 };
 
 template <bool kPaged>
-__device__ Seq sequence(const AttnArgs& a, int b, int lane) {
+constexpr int kTiles = kPaged ? 1 : 2;
+
+__device__ __forceinline__ int blocks_of(int keys) { return keys <= 0 ? 0 : (keys - 1) / kBlock + 1; }
+
+template <bool kPaged>
+__device__ Seq get_seq(const AttnArgs& a, int b, int& err) {
   Seq s;
-  s.err = 0;
+  err = 0;
   if (kPaged) {
     const int L = a.len[b];
     const int n = a.len_k ? a.len_k[b] : a.S;
     s.Lq = n;
+    s.base = L;
     s.q0 = b * a.S;
     s.k0 = 0;
-    s.Lk = L + n;
-    int err = 0;
-    if (n < 0 || n > a.S) {
-      err = SPEC_ATTN_DEVERR_LENGTH;
-      s.Lq = a.S;
-    } else if (L < 0) {
-      err = SPEC_ATTN_DEVERR_LENGTH;
-    } else if (n > 0) {
-      const long long in_pool = static_cast<long long>(L) + (a.staged ? 0 : n);
-      if (in_pool > static_cast<long long>(a.max_pages) * a.page_size) {
-        err = SPEC_ATTN_DEVERR_CAPACITY;
-      } else {
-        for (long long c = lane; c * a.page_size < in_pool; c += 32) {
-          const int p = a.bt[static_cast<long long>(b) * a.max_pages + c];
-          if (p < 0 || p >= a.num_pages) err |= SPEC_ATTN_DEVERR_PAGE;
-        }
-        if (a.parents)
-          for (int i = lane; i < n; i += 32) {
-            const int p = a.parents[static_cast<long long>(b) * a.S + i];
-            if (i == 0 ? p != -1 : (p < 0 || p >= i)) err |= SPEC_ATTN_DEVERR_TREE;
-          }
-      }
-    }
-    s.err = __reduce_or_sync(0xffffffffu, err);
+    if (n < 0 || n > a.S || (L < 0 && n > 0)) err = SPEC_ATTN_DEVERR_LENGTH;
+    else if (n > 0 && static_cast<long long>(L) + (a.staged ? 0 : n) >
+                          static_cast<long long>(a.max_pages) * a.page_size)
+      err = SPEC_ATTN_DEVERR_CAPACITY;
   } else {
     const int a0 = a.len[b], a1 = a.len[b + 1], b0 = a.len_k[b], b1 = a.len_k[b + 1];
     s.Lq = a1 - a0;
-    s.Lk = b1 - b0;
+    s.base = (b1 - b0) - s.Lq;
     s.q0 = a0;
     s.k0 = b0;
-    if (a0 < 0 || a1 < a0 || a1 > a.total_q || b0 < 0 || b1 < b0 || b1 > a.total_k) {
-      s.err = SPEC_ATTN_DEVERR_LENGTH;
-      s.Lq = 0;
-    }
+    if (a0 < 0 || a1 < a0 || a1 > a.total_q || b0 < 0 || b1 < b0 || b1 > a.total_k) err = SPEC_ATTN_DEVERR_LENGTH;
   }
+  if (err) s.Lq = 0;
+  const int t = a.tile_tokens * kTiles<kPaged>;
+  s.tiles = (s.Lq + t - 1) / t;
   return s;
 }
 
-template <typename T, int D, bool kPaged>
-__global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y;
-  const Seq s = sequence<kPaged>(a, b, lane);
-  if (s.err && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.ctrl + sv::kKvCollect, s.err);
-  const int G = a.heads / a.kv_heads;
-  const long long entry = 2ll * a.kv_heads * D;
-  for (long long r = static_cast<long long>(blockIdx.x) * kWarps + warp; r < static_cast<long long>(s.Lq) * a.heads;
-       r += static_cast<long long>(gridDim.x) * kWarps) {
-    const int i = static_cast<int>(r / a.heads), h = static_cast<int>(r % a.heads), g = h / G;
-    const long long row = s.q0 + i;
-    T* out = static_cast<T*>(a.out) + (row * a.heads + h) * D;
-    float o[E], qf[E], m = -INFINITY, l = 0.f;
-    const T* q = static_cast<const T*>(a.q) + row * a.q_stride + h * D;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o[e] = 0.f;
-      qf[e] = to_f(q[lane + 32 * e]);
+// Blocks of an item: the keys its last token sees; one (of nothing) where none is seen.
+template <bool kPaged>
+__device__ __forceinline__ int item_blocks(const AttnArgs& a, const Seq& s, int tile) {
+  if (kPaged) return a.staged ? blocks_of(s.base) + blocks_of(s.Lq) : blocks_of(s.base + s.Lq);
+  const int t = a.tile_tokens * 2;
+  const int n = blocks_of(s.base + min(s.Lq, (tile + 1) * t));
+  return n > 0 ? n : 1;
+}
+
+// sum over i < n of floor((x i + y) / m), by the Euclidean recursion.
+__device__ long long floor_sum(long long n, long long m, long long x, long long y) {
+  long long sum = 0;
+  while (n > 0) {
+    if (x >= m) {
+      sum += (n - 1) * n / 2 * (x / m);
+      x %= m;
     }
-    if (!s.err) {
-      const int L = s.Lk - s.Lq;       // keys before the first query (negative: fewer keys than queries)
-      const int last = L + i;          // the last visible key of a chain
-      // tree: the ancestors of i, as a bit per node (lane w: nodes 32w ..; at most 256 nodes)
-      unsigned anc = 0;
-      if (kPaged && a.parents)
-        for (int p = i; p >= 0; p = a.parents[static_cast<long long>(b) * a.S + p])
-          if (p / 32 == lane) anc |= 1u << (p % 32);
-      for (int j = 0; j <= last; ++j) {
-        const T *kp, *vp;
+    if (y >= m) {
+      sum += n * (y / m);
+      y %= m;
+    }
+    const long long top = x * n + y;
+    if (top < m) break;
+    n = top / m;
+    y = top % m;
+    const long long t = m;
+    m = x;
+    x = t;
+  }
+  return sum;
+}
+
+// Units (blocks and kItemUnits each) of the first t items of one head of a sequence.
+template <bool kPaged>
+__device__ long long head_units(const AttnArgs& a, const Seq& s, int t) {
+  long long sum = static_cast<long long>(t) * kItemUnits;
+  if (kPaged) return sum + static_cast<long long>(t) * item_blocks<kPaged>(a, s, 0);
+  const int span = a.tile_tokens * 2;
+  const int full = t < s.tiles ? t : s.tiles - 1;  // tiles whose last token is (i + 1) span - 1
+  int none = s.base < 0 ? -s.base / span : 0;      // tiles that see nothing: one block each
+  if (none > full) none = full;
+  sum += none + floor_sum(full - none, kBlock, span, s.base + static_cast<long long>(none + 1) * span + kBlock - 1);
+  if (t == s.tiles) sum += item_blocks<kPaged>(a, s, t - 1);
+  return sum;
+}
+
+// A place in the list of items.
+template <bool kPaged>
+struct Cursor {
+  int b, kvh, tile, n;
+  long long start;  // first unit of the item
+  Seq s;
+
+  __device__ void load(const AttnArgs& a) {
+    int err;
+    s = get_seq<kPaged>(a, b, err);
+    n = item_blocks<kPaged>(a, s, tile);
+  }
+  __device__ void next(const AttnArgs& a) {
+    start += n + kItemUnits;
+    if (++tile < s.tiles) {
+      if (!kPaged) n = item_blocks<kPaged>(a, s, tile);
+      return;
+    }
+    tile = 0;
+    if (++kvh == a.kv_heads) {
+      kvh = 0;
+      do {
+        if (++b >= a.B) return;  // behind the last item; start has reached the total
+        int err;
+        s = get_seq<kPaged>(a, b, err);
+      } while (s.tiles == 0);
+    }
+    n = item_blocks<kPaged>(a, s, 0);
+  }
+};
+
+__device__ __forceinline__ long long share(long long total, long long cta, long long grid) {
+  return total * cta / grid;
+}
+
+template <int D, bool kPaged>
+struct Shape {
+  static constexpr int kTileBytes = kBlock * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : (kPaged ? 8 : 8);
+  static constexpr int kQBytes = kTiles<kPaged> * kTileBytes;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kO = 256;  // O accumulators behind the two score tiles
+};
+
+struct Sync {
+  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], joint[3];
+  uint32_t tmem;
+  int abort;
+  int o_set[2];             // the softmax warps have written O themselves
+  unsigned spoiled[2][2][4];
+  long long u0, u1, total, start;
+  int b, kvh, tile;
+  long long scan[kThreads / 32];
+};
+
+struct PagedShared {
+  float2 ml[2][2][kBlock];        // [segment parity][warpgroup][row] (reference, sum)
+  unsigned anc[2][kBlock][9];     // [warpgroup][row] ancestors of the row's node
+};
+
+// A wait that gives up after kWaitLimitNs, or as soon as another warp has.
+__device__ __forceinline__ bool await(Sync& sh, uint64_t* bar, uint32_t parity) {
+  if (sv::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = sv::global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (sv::mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+    if (sv::global_timer_ns() - t0 > sv::kWaitLimitNs) {
+      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+// Whether a packed pair holds an infinity or a NaN (all exponent bits set).
+__device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool odd_pair(uint32_t w, __half) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+// Two products and sums in one instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  uint64_t a, b, c, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(z.x), "f"(z.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  uint64_t a, b, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+
+// kind::f16 instruction descriptor, f32 accumulators: A and B fp16 (0) or
+// bf16 (1) at bits 7 and 10, B MN-major at bit 16.
+template <typename T>
+constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t b_mn) {
+  return (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u) | (b_mn << 16) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The rank of V's load of block i among a segment's loads (cache order K0 K1 V0 K2 V1 ..).
+template <bool kPaged>
+__device__ __forceinline__ uint32_t v_rank(int i, int nb) {
+  return kPaged ? (i + 1 < nb ? 2 * i + 2 : 2 * i + 1) : 2 * i + 1;
+}
+
+// Address of the value row of a position an item sees (the slow path).
+template <typename T, int D, bool kPaged>
+__device__ const T* value_row(const AttnArgs& a, const Seq& s, int b, int kvh, bool fresh, int pos) {
+  if (!kPaged) return static_cast<const T*>(a.v) + (s.k0 + pos) * a.v_stride + kvh * D;
+  const long long entry = 2ll * a.kv_heads * D;
+  long long row;
+  const T* base;
+  if (fresh) {
+    base = static_cast<const T*>(a.staged);
+    row = static_cast<long long>(b) * a.S + pos;
+  } else {
+    base = static_cast<const T*>(a.k);
+    const int page = a.bt[static_cast<long long>(b) * a.max_pages + pos / a.page_size];
+    if (page < 0 || page >= a.num_pages) return nullptr;  // (flagged; its value is not used)
+    row = static_cast<long long>(page) * a.page_size + pos % a.page_size;
+  }
+  return base + row * entry + static_cast<long long>(a.kv_heads + kvh) * D;
+}
+
+template <typename T, int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v) {
+  // (cache: map_k is the pool's, map_v the staged entries')
+  using Sh = Shape<D, kPaged>;
+  constexpr int kNT = kTiles<kPaged>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* q_tile = smem;
+  uint8_t* ring = smem + Sh::kQBytes;
+  uint8_t* tail = ring + Sh::kStages * Sh::kTileBytes;
+  Sync& sh = *reinterpret_cast<Sync*>(tail);
+  PagedShared& ps = *reinterpret_cast<PagedShared*>(tail + (sizeof(Sync) + 15) / 16 * 16);  // (cache only)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  const long long grid = gridDim.x;
+
+  sv::griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      sv::mbar_init(&sh.full[i], 1);
+      sv::mbar_init(&sh.empty[i], 1);
+    }
+    sv::mbar_init(&sh.q_full, 1);
+    sv::mbar_init(&sh.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      sv::mbar_init(&sh.s_full[t], 1);
+      sv::mbar_init(&sh.p_full[t], 4);
+      sv::mbar_init(&sh.o_full[t], 1);
+      sv::mbar_init(&sh.o_free[t], kPaged ? 8 : 4);
+      sv::mbar_init(&sh.joint[1 + t], 4);
+    }
+    sv::mbar_init(&sh.joint[0], 8);
+    sv::fence_barrier_init();
+    sh.abort = 0;
+    a.cuts[cta].active = 0;
+  }
+  if (warp == kMmaWarp) {
+    sv::tmem_alloc(&sh.tmem, Sh::kTmemCols);
+    sv::tmem_relinquish_alloc_permit();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    sv::prefetch_tensor_map(&map_q);
+    sv::prefetch_tensor_map(&map_k);
+    sv::prefetch_tensor_map(&map_v);
+  }
+
+  // ---- this CTA's share of the units: a scan over the sequences
+  long long total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long seen = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long units = 0;
+      Seq s;
+      s.tiles = 0;
+      if (b < a.B) {
+        int err;
+        s = get_seq<kPaged>(a, b, err);
+        if (s.tiles > 0) units = head_units<kPaged>(a, s, s.tiles) * a.kv_heads;
+        if (err && pass == 0 && cta == 0) atomicOr(kPaged ? a.bad + b : a.ctrl + sv::kKvCollect, err);
+      }
+      long long x = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = x;
+      __syncthreads();
+      long long before = seen, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh.scan[w];
+        sum += sh.scan[w];
+      }
+      before += x - units;
+      seen += sum;
+      if (pass == 0 && b0 + kThreads < a.B) continue;  // the total is not known yet
+      if (pass == 0) total = seen;
+      if (pass == 0 && a.B > kThreads) break;          // find the start in a second pass
+      const long long u0 = share(total, cta, grid);
+      if (units > 0 && before <= u0 && u0 < before + units) {
+        const long long per_head = units / a.kv_heads, r = (u0 - before) % per_head;
+        int lo = 0, hi = s.tiles;  // the last tile that starts at or before r
         if (kPaged) {
-          if (j >= L && a.parents && !(__shfl_sync(0xffffffffu, anc, (j - L) / 32) >> ((j - L) % 32) & 1u)) continue;
-          long long at;
-          const T* base;
-          if (a.staged && j >= L) {
-            base = static_cast<const T*>(a.staged);
-            at = static_cast<long long>(b) * a.S + (j - L);
-          } else {
-            base = static_cast<const T*>(a.k);
-            at = static_cast<long long>(a.bt[static_cast<long long>(b) * a.max_pages + j / a.page_size]) * a.page_size +
-                 j % a.page_size;
-          }
-          kp = base + at * entry + g * D;
-          vp = kp + a.kv_heads * D;
+          lo = static_cast<int>(r / (item_blocks<kPaged>(a, s, 0) + kItemUnits));
         } else {
-          kp = static_cast<const T*>(a.k) + (s.k0 + j) * a.k_stride + g * D;
-          vp = static_cast<const T*>(a.v) + (s.k0 + j) * a.v_stride + g * D;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (head_units<kPaged>(a, s, mid) <= r) lo = mid;
+            else hi = mid;
+          }
         }
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dot += qf[e] * to_f(kp[lane + 32 * e]);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        dot *= a.scale;
-        const float top = fmaxf(m, dot);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float keep = expf(m - ref), w = expf(dot - ref);
-        l = l * keep + w;
-        m = top;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * to_f(vp[lane + 32 * e]);
+        sh.b = b;
+        sh.kvh = static_cast<int>((u0 - before) / per_head);
+        sh.tile = lo;
+        sh.start = u0 - r + (lo ? head_units<kPaged>(a, s, lo) : 0);
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) from_f(out[lane + 32 * e], l == 0.f ? 0.f : o[e] * inv);
-    if (a.lse && lane == 0) a.lse[row * a.heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+    if (a.B <= kThreads) break;
   }
+  if (tid == 0) {
+    sh.u0 = share(total, cta, grid);
+    sh.u1 = share(total, cta + 1, grid);
+    sh.total = total;
+  }
+  if (kPaged && a.parents) {  // trees are checked once per sequence
+    for (int b = cta; b < a.B; b += gridDim.x) {
+      int err;
+      const Seq s = get_seq<kPaged>(a, b, err);
+      for (int i = tid; i < s.Lq; i += kThreads) {
+        const int p = a.parents[static_cast<long long>(b) * a.S + i];
+        if (i == 0 ? p != -1 : (p < 0 || p >= i)) atomicOr(a.bad + b, SPEC_ATTN_DEVERR_TREE);
+      }
+    }
+  }
+  sv::tc_fence_before_sync();
   __syncthreads();
-  if (threadIdx.x == 0 && sv::kv_last_cta(a.ctrl)) sv::kv_publish(a.ctrl);
+  sv::tc_fence_after_sync();
+  const long long u0 = sh.u0, u1 = sh.u1;
+  const uint32_t tmem = sh.tmem;
+
+  Cursor<kPaged> at = {};
+  at.start = u1;  // no share: nothing to walk
+  if (u0 < u1) {
+    at.b = sh.b;
+    at.kvh = sh.kvh;
+    at.tile = sh.tile;
+    at.start = sh.start;
+    at.load(a);
+  }
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------- loads
+    uint32_t loads = 0, segs = 0;
+    const uint64_t keep = sv::l2_policy_evict_last(), once = sv::l2_policy_evict_first();
+    const uint64_t policy = kPaged && a.S * a.G <= kBlock ? once : keep;
+    // takes the next slot of the ring (all lanes; lane 0 waits and announces the bytes)
+    auto slot_of = [&]() -> uint8_t* {
+      const uint32_t slot = loads % Sh::kStages;
+      if (lane == 0) {
+        ok = ok && await(sh, &sh.empty[slot], (loads / Sh::kStages & 1) ^ 1);
+        if (ok) sv::mbar_arrive_expect_tx(&sh.full[slot], Sh::kTileBytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      return ring + slot * Sh::kTileBytes;
+    };
+    auto bar_of = [&]() { return &sh.full[loads % Sh::kStages]; };
+    for (; ok && at.start < u1; at.next(a)) {
+      const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
+      const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+      if (hi <= lo) continue;
+      auto load_q = [&]() {
+        if (lane == 0 && ok) {
+          ok = segs == 0 || await(sh, &sh.q_empty, (segs - 1) & 1);
+          if (ok) {
+            const int tok = at.s.q0 + at.tile * a.tile_tokens * kNT;
+            sv::mbar_arrive_expect_tx(&sh.q_full, kNT * a.tile_tokens * a.G * D * 2);
+            for (int t = 0; t < kNT; ++t)
+              for (int h = 0; h < D / 64; ++h)
+                sv::tma_load_3d(q_tile + t * Sh::kTileBytes + h * (kBlock * 128), &map_q, &sh.q_full, h * 64,
+                                at.kvh * a.G, tok + t * a.tile_tokens, once);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      };
+      if (kPaged) {
+        const int committed = a.staged ? blocks_of(at.s.base) : at.n;  // blocks read from the pool
+        const int limit = a.staged ? at.s.base : at.s.base + at.s.Lq;
+        const int* table = a.bt + static_cast<long long>(at.b) * a.max_pages;
+        const int x_k = at.kvh * D, x_v = (a.kv_heads + at.kvh) * D;
+        int r0[4], r1[4];  // this lane's four rows of the block before, of this block
+        auto rows_of = [&](int j, int (&r)[4]) {
+          if (j >= committed) {
+            const int i0 = (j - committed) * kBlock + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = i0 + e < at.s.Lq ? at.b * a.S + i0 + e : a.B * a.S;
+            return;
+          }
+          const int p0 = j * kBlock + 4 * lane;
+          int col = p0 / a.page_size, slot = p0 - col * a.page_size;
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[e] = a.num_pages * a.page_size;
+            if (p0 + e < limit) {
+              const int page = table[col];
+              if (page >= 0 && page < a.num_pages) r[e] = page * a.page_size + slot;
+              else bad = true;
+            }
+            if (++slot == a.page_size) {
+              slot = 0;
+              ++col;
+            }
+          }
+          if (bad) atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
+        };
+        auto gather = [&](int j, const int (&r)[4], int x) {
+          uint8_t* dst = slot_of();
+          if (!ok) return;
+          const CUtensorMap* map = j >= committed ? &map_v : &map_k;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            sv::tma_gather4(dst + h * (kBlock * 128) + lane * 512, map, bar_of(), x + h * 64, r[0], r[1], r[2], r[3],
+                            policy);
+          ++loads;
+        };
+        rows_of(lo, r0);
+        gather(lo, r0, x_k);
+        load_q();
+        for (int j = lo; ok && j < hi; ++j) {
+          if (j + 1 < hi) {
+            rows_of(j + 1, r1);
+            gather(j + 1, r1, x_k);
+          }
+          if (ok) gather(j, r0, x_v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r0[e] = r1[e];
+        }
+      } else {
+        for (int j = lo; ok && j < hi; ++j) {
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            uint8_t* dst = slot_of();
+            if (ok && lane == 0)
+              for (int h = 0; h < D / 64; ++h)
+                sv::tma_load_3d(dst + h * (kBlock * 128), kv ? &map_v : &map_k, bar_of(), h * 64, at.kvh,
+                                static_cast<int>(at.s.k0) + j * kBlock, policy);
+            ++loads;
+            if (j == lo && kv == 0) load_q();
+          }
+        }
+      }
+      ++segs;
+    }
+    if (!ok) {  // leave no copy in flight
+      if (lane == 0) {
+        const uint32_t first = loads > Sh::kStages ? loads - Sh::kStages : 0;
+        for (uint32_t i = first; i < loads; ++i) sv::mbar_wait(&sh.full[i % Sh::kStages], i / Sh::kStages & 1);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // --------------------------------------------------------------- MMA
+    if (lane == 0) {
+      uint32_t loads = 0, segs = 0, p_cnt[2] = {0, 0}, used[2] = {0, 0};
+      constexpr uint32_t kIdS = idesc<T>(kBlock, kBlock, 0), kIdO = idesc<T>(kBlock, D, 1);
+      const uint32_t ring_addr = sv::smem_u32(ring), q_addr = sv::smem_u32(q_tile);
+      auto arrived = [&]() -> uint32_t {  // waits for the next load; its address
+        const uint32_t slot = loads % Sh::kStages;
+        ok = ok && await(sh, &sh.full[slot], loads / Sh::kStages & 1);
+        sv::tc_fence_after_sync();
+        return ring_addr + slot * Sh::kTileBytes;
+      };
+      auto scores = [&](int t, uint32_t k_addr) {
+        const uint32_t qa = q_addr + (kPaged ? 0 : t * Sh::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * (kBlock * 128) + (k % 4) * 32;
+          sv::mma_bf16_ss(tmem + t * kBlock, sv::smem_desc_k_sw128(qa + off), sv::smem_desc_k_sw128(k_addr + off), kIdS,
+                          k > 0);
+        }
+        sv::mma_commit(&sh.s_full[t]);
+      };
+      // P V of one block; waits for P and, first, for O to be free
+      auto values = [&](int t, uint32_t v_addr, bool first) {
+        if (first && used[t] > 0) ok = ok && await(sh, &sh.o_free[t], (used[t] - 1) & 1);
+        ok = ok && await(sh, &sh.p_full[t], p_cnt[t] & 1);
+        ++p_cnt[t];
+        if (!ok) return;
+        sv::tc_fence_after_sync();
+        const bool fresh = first && !*reinterpret_cast<volatile int*>(&sh.o_set[t]);
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)
+          sv::mma_f16_ts(tmem + Sh::kO + t * D, tmem + t * kBlock + k * 8,
+                         sv::smem_desc_mn_sw128(v_addr + k * 2048, kBlock * 128), kIdO, !(fresh && k == 0));
+      };
+      for (; ok && at.start < u1; at.next(a)) {
+        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
+        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+        const int nb = hi - lo;
+        if (nb <= 0) continue;
+        ok = ok && await(sh, &sh.q_full, segs & 1);
+        if (kPaged) {
+          for (int i = 0; i < 2 && i < nb && ok; ++i) {
+            const uint32_t k_addr = arrived();
+            if (!ok) break;
+            scores(i, k_addr);
+            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+          }
+          if (nb <= 2) sv::mma_commit(&sh.q_empty);
+          for (int i = 0; ok && i < nb; ++i) {
+            const int t = i & 1;
+            const uint32_t v_addr = arrived();
+            if (ok) values(t, v_addr, i < 2);
+            if (!ok) break;
+            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+            if (i + 2 >= nb) sv::mma_commit(&sh.o_full[t]);
+            if (i + 2 < nb) {
+              const uint32_t k_addr = arrived();
+              if (!ok) break;
+              scores(t, k_addr);
+              sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+              if (i + 3 == nb) sv::mma_commit(&sh.q_empty);
+            }
+          }
+          ++used[0];
+          if (nb > 1) ++used[1];
+        } else {
+          const bool two = at.s.Lq - at.tile * a.tile_tokens * 2 > a.tile_tokens;
+          uint32_t k_addr = arrived();
+          if (ok) {
+            scores(0, k_addr);
+            if (two) scores(1, k_addr);
+            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+            if (nb == 1) sv::mma_commit(&sh.q_empty);
+          }
+          for (int i = 0; ok && i < nb; ++i) {
+            const uint32_t v_addr = arrived(), v_slot = loads++ % Sh::kStages;
+            if (ok) values(0, v_addr, i == 0);
+            if (!ok) break;
+            if (i + 1 == nb) sv::mma_commit(&sh.o_full[0]);
+            uint32_t k_slot = 0;
+            if (i + 1 < nb) {
+              k_addr = arrived();
+              k_slot = loads++ % Sh::kStages;
+              if (!ok) break;
+              scores(0, k_addr);
+            }
+            if (two) {
+              values(1, v_addr, i == 0);
+              if (!ok) break;
+            }
+            sv::mma_commit(&sh.empty[v_slot]);
+            if (two && i + 1 == nb) sv::mma_commit(&sh.o_full[1]);
+            if (i + 1 < nb) {
+              if (two) scores(1, k_addr);
+              sv::mma_commit(&sh.empty[k_slot]);
+              if (i + 2 == nb) sv::mma_commit(&sh.q_empty);
+            }
+          }
+          ++used[0];
+          if (two) ++used[1];
+        }
+        ++segs;
+      }
+    }
+    __syncwarp();
+  } else if (warp < kMmaWarp) {
+    // ----------------------------------------------------------- softmax
+    const int t = warp >> 2, row = tid & (kBlock - 1);
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
+    const uint32_t s_addr = tmem + t * kBlock + lanes;
+    const float c2 = a.scale_log2;
+    uint32_t loads = 0, s_cnt = 0, used[2] = {0, 0}, j_cnt[3] = {0, 0, 0}, merges = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // one answer for the whole warp
+      ok = __all_sync(0xffffffffu, ok && await(sh, bar, parity));
+    };
+    auto meet = [&](int g) {  // all warps of a group (0: both warpgroups, 1 + t: this one)
+      __syncwarp();
+      if (lane == 0) sv::mbar_arrive(&sh.joint[g]);
+      wait(&sh.joint[g], j_cnt[g] & 1);
+      ++j_cnt[g];
+    };
+    for (; ok && at.start < u1; at.next(a)) {
+      const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
+      const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+      const int nb = hi - lo;
+      if (nb <= 0) continue;
+      const Seq& s = at.s;
+      const int item_tok = at.tile * a.tile_tokens * kNT;
+      const int tok0 = item_tok + (kPaged ? 0 : t * a.tile_tokens);
+      const int rows = max(0, min(a.tile_tokens, s.Lq - tok0)) * a.G;
+      const bool both = kPaged ? nb > 1 : s.Lq - item_tok > a.tile_tokens;  // the second score tile is in use
+      if (t == 0 && row == 0 && lo > 0) {
+        Cut cut;
+        cut.start = at.start;
+        cut.total = sh.total;
+        cut.b = at.b;
+        cut.kvh = at.kvh;
+        cut.tile = at.tile;
+        cut.n = at.n;
+        int p = cta - 1;
+        while (share(cut.total, p, grid) == u0) --p;  // (CTAs without a share)
+        cut.first = p;
+        cut.active = share(cut.total, p, grid) - at.start - kItemUnits <= 0;
+        a.cuts[cta] = cut;
+      }
+      if (t == 1 && !both) {
+        loads += 2 * nb;
+        ++used[0];
+        continue;
+      }
+      const bool alive = (row & ~31) < rows;  // the warp has a row
+      const int i_tok = tok0 + row / a.G;     // this row's token
+      const int committed = kPaged && a.staged ? blocks_of(s.base) : at.n;
+      const bool tree = kPaged && a.parents != nullptr;
+      if (tree && alive) {
+        unsigned* anc = ps.anc[t][row];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) anc[w] = 0;
+        int p = min(i_tok, s.Lq - 1);
+        while (p >= 0) {
+          anc[p >> 5] |= 1u << (p & 31);
+          const int up = a.parents[static_cast<long long>(at.b) * a.S + p];
+          p = up < p ? up : -1;  // (a bad parent is flagged; the walk still ends)
+        }
+      }
+      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of its weights
+      float top = -INFINITY;             // the same reference as a score
+
+      for (int i = kPaged ? t : 0; ok && i < nb; i += kPaged ? 2 : 1) {
+        const bool first = i < (kPaged ? 2 : 1);
+        const int j = lo + i;
+        // the block's first position (fresh: index among the new entries), how far this row and the item's first
+        // row see into it
+        const bool fresh = j >= committed;
+        const int pos0 = (fresh ? j - committed : j) * kBlock;
+        int seen, least;
+        if (kPaged && a.staged) {
+          seen = fresh ? i_tok + 1 - pos0 : s.base - pos0;
+          least = fresh ? (tree ? 0 : item_tok + 1 - pos0) : s.base - pos0;
+        } else {
+          seen = s.base + i_tok + 1 - pos0;
+          least = s.base + (tree ? 0 : item_tok + 1) - pos0;
+        }
+        const bool masked = least < kBlock;
+        const bool look = masked && (!kPaged || (s.Lq > 1 && (fresh || !a.staged)));
+        wait(&sh.s_full[t], s_cnt & 1);
+        ++s_cnt;
+        if (!ok) break;
+        sv::tc_fence_after_sync();
+        unsigned spoil[4] = {0, 0, 0, 0};
+        if (look) {
+          const bool pair = !kPaged && both;
+          const int g = pair ? 0 : 1 + t, part = pair ? t : 0, box = pair ? 0 : t;
+          const uint32_t rank = loads + v_rank<kPaged>(i, nb), slot = rank % Sh::kStages;
+          wait(&sh.full[slot], rank / Sh::kStages & 1);
+          uint8_t* vrow = ring + slot * Sh::kTileBytes + row * 128;
+          const int chunks = pair ? D / 16 : D / 8, c0 = part * chunks;
+          bool odd = false;
+          if (ok)
+            for (int c = 0; c < chunks; ++c) {
+              const int cc = c0 + c;
+              const uint4 w = *reinterpret_cast<const uint4*>(vrow + (cc >> 3) * (kBlock * 128) +
+                                                              (((cc & 7) ^ (row & 7)) << 4));
+              odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
+            }
+          const unsigned word = __ballot_sync(0xffffffffu, odd);
+          if (lane == 0) sh.spoiled[box][part][warp & 3] = word;
+          meet(g);
+          if (!ok) break;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            spoil[w] = *reinterpret_cast<volatile unsigned*>(&sh.spoiled[box][0][w]) |
+                       (pair ? *reinterpret_cast<volatile unsigned*>(&sh.spoiled[box][1][w]) : 0u);
+          const unsigned own = (warp & 2) ? ((warp & 1) ? spoil[3] : spoil[2]) : ((warp & 1) ? spoil[1] : spoil[0]);
+          if (own >> lane & 1u) {
+            for (int c = 0; c < chunks; ++c) {
+              const int cc = c0 + c;
+              *reinterpret_cast<uint4*>(vrow + (cc >> 3) * (kBlock * 128) + (((cc & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            sv::fence_proxy_async_smem();
+          }
+          meet(g);
+          if (!ok) break;
+          if (!kPaged) {  // keys behind the sequence's are other sequences': zeroed, not added
+            const int keys = s.base + s.Lq - pos0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              spoil[w] &= keys >= 32 * (w + 1) ? 0xffffffffu : (keys <= 32 * w ? 0u : (1u << (keys - 32 * w)) - 1u);
+          }
+        }
+        const bool spoils = (spoil[0] | spoil[1] | spoil[2] | spoil[3]) != 0;
+        if (first && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
+        if (alive) {
+          unsigned word[4];
+          if (masked) {
+            if (tree && (fresh || !a.staged)) {
+              const unsigned* anc = ps.anc[t][row];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                // bits idx0 .. idx0 + 31 of the ancestors; everything before the new entries is seen
+                const int idx0 = pos0 + 32 * w - (fresh && a.staged ? 0 : s.base);
+                const int k = idx0 >> 5, shift = idx0 & 31;
+                const unsigned b0 = k < 0 ? 0xffffffffu : (k < 8 ? anc[k] : 0u);
+                const unsigned b1 = k + 1 < 0 ? 0xffffffffu : (k + 1 < 8 ? anc[k + 1] : 0u);
+                word[w] = __funnelshift_r(b0, b1, shift);
+              }
+            } else {
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                word[w] = seen >= 32 * (w + 1) ? 0xffffffffu : (seen <= 32 * w ? 0u : (1u << (seen - 32 * w)) - 1u);
+            }
+          }
+          // 64 scores, -infinity where the row must not see the key
+          auto scores = [&](int h, float (&x)[64]) {
+            sv::tmem_load_64(s_addr + 64 * h, x);
+            if (!masked) return;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!(word[2 * h + (c >> 5)] >> (c & 31) & 1u)) x[c] = -INFINITY;
+          };
+          float blk = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[64];
+            scores(h, x);
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            blk = fmaxf(blk, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          }
+          // raise the reference where a weight would exceed 2^kSlack
+          const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+          const float was = ref;
+          if (raise) {
+            top = blk;
+            ref = top * c2;
+          }
+          const bool lift = !first && __any_sync(0xffffffffu, raise);
+          const float off = ref == -INFINITY ? 0.f : -ref;
+          if (lift) {
+            const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
+            sum *= f;
+            const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              sv::tmem_load_32(o_addr + c, o);
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+              sv::tmem_store_32(o_addr + c, w);
+            }
+            sv::tmem_wait_st();
+          }
+          if (spoils) {  // rare: values that are infinite or not a number, for the rows that see them
+            const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
+            if (first) {
+              if (used[t] > 0) wait(&sh.o_free[t], (used[t] - 1) & 1);
+              sv::tc_fence_after_sync();
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = 0;
+              for (int c = 0; c < D; c += 32) sv::tmem_store_32(o_addr + c, w);
+              sv::tmem_wait_st();
+            }
+#pragma unroll 1
+            for (int c = 0; c < kBlock; ++c) {
+              const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
+              if (!(sw >> (c & 31) & 1u)) continue;
+              const unsigned vw = c < 64 ? (c < 32 ? word[0] : word[1]) : (c < 96 ? word[2] : word[3]);
+              const bool mine = vw >> (c & 31) & 1u;
+              const float sc = sv::tmem_load_1(s_addr + c);
+              const float p = exp2_approx(fmaf(sc, c2, off));
+              const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                float o[32];
+                sv::tmem_load_32(o_addr + d, o);
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  w[e] = __float_as_uint(mine && v != nullptr ? o[e] + p * to_f(v[d + e]) : o[e]);
+                sv::tmem_store_32(o_addr + d, w);
+                sv::tmem_wait_st();
+              }
+            }
+          }
+          const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // the scores are read a second time rather than held: P's 32 columns of a half lie below the scores still
+          // to be read
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[64];
+            scores(h, x);
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int c = 2 * e;
+              float2 z = fma2(make_float2(x[c], x[c + 1]), cc, oo);
+              z.x = exp2_approx(z.x);
+              z.y = exp2_approx(z.y);
+              acc[e & 1] = add2(acc[e & 1], z);
+              w[e] = pack2(z.x, z.y, T());
+            }
+            sv::tmem_store_32(s_addr + h * 32, w);
+          }
+          const float2 both_acc = add2(acc[0], acc[1]);
+          sum += both_acc.x + both_acc.y;
+          sv::tmem_wait_st();
+        }
+        sv::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) sv::mbar_arrive(&sh.p_full[t]);
+      }
+      loads += 2 * nb;
+      if (!ok) break;
+
+      // ---- end of the segment: normalise and write, or leave partial rows
+      const bool whole = lo == 0 && hi == at.n;
+      const long long slot = (static_cast<long long>(cta) * 2 + (lo > 0 ? 0 : 1)) * (kNT * kBlock);
+      int d0 = 0, d1 = D;
+      float f0 = 1.f, f1 = 0.f, all = sum, base2 = ref;
+      if (kPaged) {
+        if (both) {
+          float2(&ml)[2][kBlock] = ps.ml[merges & 1];
+          ++merges;
+          ml[t][row] = make_float2(ref, sum);
+          meet(0);
+          if (!ok) break;
+          const float2 m0 = ml[0][row], m1 = ml[1][row];
+          base2 = fmaxf(m0.x, m1.x);
+          f0 = m0.x == -INFINITY ? 0.f : exp2_approx(m0.x - base2);
+          f1 = m1.x == -INFINITY ? 0.f : exp2_approx(m1.x - base2);
+          all = m0.y * f0 + m1.y * f1;
+          d0 = t * (D / 2);
+          d1 = d0 + D / 2;
+        }
+        wait(&sh.o_full[0], used[0] & 1);
+        if (both) wait(&sh.o_full[1], used[1] & 1);
+      } else {
+        wait(&sh.o_full[t], used[t] & 1);
+      }
+      if (!ok) break;
+      sv::tc_fence_after_sync();
+      if (alive) {
+        const bool mine = row < rows;
+        const long long orow = (static_cast<long long>(s.q0) + i_tok) * a.heads + at.kvh * a.G + row % a.G;
+        const float inv = whole ? (all == 0.f ? 0.f : 1.f / all) : 1.f;
+        const bool none = all == 0.f;
+        const int prow = kPaged ? row : t * kBlock + row;
+        const uint32_t o_addr = tmem + Sh::kO + (kPaged ? 0 : t * D) + lanes;
+#pragma unroll 1
+        for (int d = d0; d < d1; d += 32) {
+          float o[32];
+          sv::tmem_load_32(o_addr + d, o);
+          if (kPaged && both) {
+            float o2[32];
+            sv::tmem_load_32(o_addr + D + d, o2);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+          }
+          if (!mine) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = none ? 0u : pack2(o[8 * e + 2 * k] * inv, o[8 * e + 2 * k + 1] * inv, T());
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (slot + prow) * D + d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (mine && d0 == 0) {
+          if (!whole) a.part_ml[slot + prow] = make_float2(base2, all);
+          else if (a.lse) a.lse[orow] = none ? -INFINITY : (base2 + log2f(all)) * kLn2;
+        }
+      }
+      sv::tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPaged) {
+          sv::mbar_arrive(&sh.o_free[0]);
+          sv::mbar_arrive(both ? &sh.o_free[1] : &sh.o_free[0]);
+        } else {
+          sv::mbar_arrive(&sh.o_free[t]);
+        }
+      }
+      ++used[0];
+      if (both) ++used[1];
+    }
+  }
+
+  __syncwarp();
+  sv::tc_fence_before_sync();
+  __syncthreads();
+  sv::tc_fence_after_sync();
+  if (warp == kMmaWarp) sv::tmem_dealloc(tmem, Sh::kTmemCols);
+  if (tid == 0 && sh.abort) atomicOr(a.ctrl + sv::kKvCollect, SPEC_ATTN_DEVERR_TIMEOUT);
+}
+
+// Joins the partial rows of every item that was cut, zeroes the rows of
+// sequences found bad, and publishes the error word.  CTA (c, y) takes every
+// kJoinSplit-th group of rows of the item whose first cut CTA c begins with.
+// A few partial rows (at most one item per CTA of the main kernel) of L2
+// traffic: bound by latency.
+template <typename T, int D, bool kPaged>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int main_grid) {
+  constexpr int kNT = kTiles<kPaged>, kE = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sv::griddep_wait();
+  const Cut cut = a.cuts[blockIdx.x];
+  if (cut.active && !(kPaged && a.bad[cut.b])) {
+    int err;
+    const Seq s = get_seq<kPaged>(a, cut.b, err);
+    const int tok0 = cut.tile * a.tile_tokens * kNT;
+    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < kNT * kBlock; r += kJoinSplit * (kJoinThreads / 32)) {
+      const int sub = r / kBlock, in = r % kBlock, tok = tok0 + sub * a.tile_tokens + in / a.G;
+      if (in >= a.tile_tokens * a.G || tok >= s.Lq) continue;
+      float o[kE], ref = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] = 0.f;
+      for (int p = cut.first; p < main_grid; ++p) {
+        const long long from = share(cut.total, p, main_grid), to = share(cut.total, p + 1, main_grid);
+        if (from == to) continue;
+        if (p > cut.first && from - cut.start - kItemUnits >= cut.n) break;
+        const long long at = (static_cast<long long>(p) * 2 + (p == cut.first ? 1 : 0)) * (kNT * kBlock) + r;
+        const float2 ml = a.part_ml[at];
+        if (ml.x == -INFINITY) continue;  // this piece saw no key
+        const float top = fmaxf(ref, ml.x);
+        const float f = ref == -INFINITY ? 0.f : exp2_approx(ref - top), g = exp2_approx(ml.x - top);
+        sum = sum * f + ml.y * g;
+        ref = top;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const float x = a.part_o[at * D + lane * kE + e];
+          o[e] = (f == 0.f ? 0.f : o[e] * f) + (g == 0.f ? 0.f : x * g);
+        }
+      }
+      const bool none = sum == 0.f;
+      const float inv = none ? 0.f : 1.f / sum;
+      const long long orow = (static_cast<long long>(s.q0) + tok) * a.heads + cut.kvh * a.G + in % a.G;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + orow * D + lane * kE);
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) dst[e / 2] = none ? 0u : pack2(o[e] * inv, o[e + 1] * inv, T());
+      if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : (ref + log2f(sum)) * kLn2;
+    }
+  }
+  if (kPaged) {
+    for (int b = blockIdx.x * kJoinSplit + blockIdx.y; b < a.B; b += gridDim.x * kJoinSplit) {
+      if (!a.bad[b]) continue;
+      const int n = a.len_k ? a.len_k[b] : a.S;
+      const long long rows = static_cast<long long>(n < 0 || n > a.S ? a.S : n) * a.heads;
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<long long>(b) * a.S * a.heads * D);
+      for (long long i = threadIdx.x; i < rows * D / 8; i += kJoinThreads) dst[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (long long i = threadIdx.x; i < rows; i += kJoinThreads)
+          a.lse[static_cast<long long>(b) * a.S * a.heads + i] = -INFINITY;
+    }
+  }
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = sv::kv_last_cta(a.ctrl);
+  __syncthreads();
+  if (!s_last) return;
+  if (kPaged)
+    for (int b = threadIdx.x; b < a.B; b += kJoinThreads) {
+      const int bits = a.bad[b];
+      if (bits) {
+        atomicOr(a.ctrl + sv::kKvCollect, bits);
+        a.bad[b] = 0;
+      }
+    }
+  __syncthreads();
+  if (threadIdx.x == 0) sv::kv_publish(a.ctrl);
 }
 
 // --------------------------------------------------------------------- host
@@ -200,31 +1137,110 @@ bool prompt_dims_ok(const spec_prompt_dims& d) {
          stride_ok(d.v_stride, d.kv_heads, d.head_dim);
 }
 
-size_t workspace_size() { return sv::kKvCtrlBytes; }
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Layout {
+  size_t bad, cuts, part_ml, part_o, total;
+};
+
+Layout layout(int B, int head_dim, int tiles) {
+  Layout l;
+  const size_t rows = static_cast<size_t>(kMaxGrid) * 2 * tiles * kBlock;
+  l.bad = sv::kKvCtrlBytes;
+  l.cuts = l.bad + up(4 * static_cast<size_t>(B));
+  l.part_ml = l.cuts + up(sizeof(Cut) * kMaxGrid);
+  l.part_o = l.part_ml + up(sizeof(float2) * rows);
+  l.total = l.part_o + up(sizeof(float) * rows * head_dim);
+  return l;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// A 16-bit tensor with boxes of 64 elements (128 bytes, 128-byte swizzle) by box_y by box_z, zeros outside.
+bool encode(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
+            uint32_t box_y, uint32_t box_z) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {dim[0], dim[1], dim[2]}, strides[2] = {stride[0], stride[1]};
+  const cuuint32_t box[3] = {64, box_y, box_z}, step[3] = {1, 1, 1};
+  return fn(map, dtype == SPEC_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tokens(CUtensorMap* map, int dtype, const void* base, int head_dim, int heads, int64_t tokens,
+                   int64_t stride, int box_heads, int box_tokens) {
+  return encode(map, dtype, base, 3,
+                {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)},
+                {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(stride) * 2}, box_heads, box_tokens);
+}
+
+bool encode_entries(CUtensorMap* map, int dtype, const void* base, int64_t entry, int64_t rows) {
+  return encode(map, dtype, base, 2, {static_cast<uint64_t>(entry), static_cast<uint64_t>(rows), 1},
+                {static_cast<uint64_t>(entry) * 2, 0}, 1, 1);
+}
+
+template <typename T, int D, bool kPaged>
+spec_status launch(const AttnArgs& a, const CUtensorMap (&maps)[3], const sv::DeviceInfo& dev, cudaStream_t s) {
+  using Sh = Shape<D, kPaged>;
+  constexpr size_t kBytes = 1024 + Sh::kQBytes + Sh::kStages * Sh::kTileBytes + (sizeof(Sync) + 15) / 16 * 16 +
+                            (kPaged ? sizeof(PagedShared) : 0);
+  static_assert(kBytes <= 232448, "shared memory of one CTA");
+  static_assert(kBytes > 116 * 1024, "one CTA per SM: it takes all of the tensor memory");
+  static bool done[64] = {false};
+  if (!done[dev.device]) {
+    if (cudaFuncSetAttribute(attn_kernel<T, D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kBytes)) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    done[dev.device] = true;
+  }
+  const int grid = dev.sm_count < kMaxGrid ? dev.sm_count : kMaxGrid;
+  attn_kernel<T, D, kPaged><<<grid, kThreads, kBytes, s>>>(a, maps[0], maps[1], maps[2]);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  if (sv::launch_dependent(attn_join_kernel<T, D, kPaged>, dim3(grid, kJoinSplit), dim3(kJoinThreads), s, a, grid) !=
+      cudaSuccess)
+    return SPEC_ERR_CUDA;
+  return SPEC_OK;
+}
 
 template <bool kPaged>
-spec_status launch(const AttnArgs& a, int head_dim, int dtype, int rows, cudaStream_t s) {
-  const long long warps = static_cast<long long>(rows) * a.heads;
-  const long long want = (warps + kWarps - 1) / kWarps;
-  const dim3 grid(static_cast<unsigned>(want < 4096 ? want : 4096), a.B);
-  if (dtype == SPEC_ATTN_BF16) {
-    if (head_dim == 64) attn_rows_kernel<__nv_bfloat16, 64, kPaged><<<grid, kThreads, 0, s>>>(a);
-    else attn_rows_kernel<__nv_bfloat16, 128, kPaged><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (head_dim == 64) attn_rows_kernel<__half, 64, kPaged><<<grid, kThreads, 0, s>>>(a);
-    else attn_rows_kernel<__half, 128, kPaged><<<grid, kThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+spec_status launch(AttnArgs& a, const CUtensorMap (&maps)[3], int head_dim, int dtype, const sv::DeviceInfo& dev,
+                   void* workspace, cudaStream_t s) {
+  const Layout l = layout(a.B, head_dim, kTiles<kPaged>);
+  char* ws = static_cast<char*>(workspace);
+  a.ctrl = reinterpret_cast<int*>(ws);
+  a.bad = reinterpret_cast<int*>(ws + l.bad);
+  a.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
+  a.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+  a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  if (dtype == SPEC_ATTN_BF16)
+    return head_dim == 64 ? launch<__nv_bfloat16, 64, kPaged>(a, maps, dev, s)
+                          : launch<__nv_bfloat16, 128, kPaged>(a, maps, dev, s);
+  return head_dim == 64 ? launch<__half, 64, kPaged>(a, maps, dev, s) : launch<__half, 128, kPaged>(a, maps, dev, s);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t spec_kv_attention_workspace_bytes(spec_kv_attn_dims dims) { return kv_dims_ok(dims) ? workspace_size() : 0; }
+size_t spec_kv_attention_workspace_bytes(spec_kv_attn_dims dims) {
+  return kv_dims_ok(dims) ? layout(dims.B, dims.head_dim, kTiles<true>).total : 0;
+}
 
 size_t spec_prompt_attention_workspace_bytes(spec_prompt_dims dims) {
-  return prompt_dims_ok(dims) ? workspace_size() : 0;
+  return prompt_dims_ok(dims) ? layout(dims.B, dims.head_dim, kTiles<false>).total : 0;
 }
 
 spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* block_table, const int32_t* seq_len,
@@ -238,7 +1254,7 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
       misaligned(workspace, 16) || misaligned(block_table, 4) || misaligned(seq_len, 4) || misaligned(parents, 4) ||
       misaligned(q_len, 4) || misaligned(out_lse, 4))
     return SPEC_ERR_ALIGN;
-  if (workspace_bytes < workspace_size()) return SPEC_ERR_WORKSPACE;
+  if (workspace_bytes < spec_kv_attention_workspace_bytes(dims)) return SPEC_ERR_WORKSPACE;
   sv::DeviceInfo dev;
   const int st = sv::current_device(dev);
   if (st != SPEC_OK) return static_cast<spec_status>(st);
@@ -252,17 +1268,24 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   a.parents = parents;
   a.out = out;
   a.lse = out_lse;
-  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
   a.B = dims.B;
   a.S = dims.S;
   a.heads = dims.heads;
   a.kv_heads = dims.kv_heads;
+  a.G = dims.heads / dims.kv_heads;
   a.page_size = dims.page_size;
   a.num_pages = dims.num_pages;
   a.max_pages = dims.max_pages;
-  a.q_stride = dims.q_stride;
-  a.ctrl = static_cast<int*>(workspace);
-  return launch<true>(a, dims.head_dim, dims.dtype, dims.S, reinterpret_cast<cudaStream_t>(stream));
+  a.tile_tokens = kBlock / a.G;
+  const int64_t entry = 2ll * dims.kv_heads * dims.head_dim, tokens = static_cast<int64_t>(dims.B) * dims.S;
+  CUtensorMap maps[3];
+  if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens) ||
+      !encode_entries(&maps[1], dims.dtype, pool, entry, static_cast<int64_t>(dims.num_pages) * dims.page_size) ||
+      !encode_entries(&maps[2], dims.dtype, staged ? staged : pool, entry,
+                      staged ? tokens : static_cast<int64_t>(dims.num_pages) * dims.page_size))
+    return SPEC_ERR_CUDA;
+  return launch<true>(a, maps, dims.head_dim, dims.dtype, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 spec_status spec_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu_q,
@@ -274,7 +1297,7 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16) || misaligned(workspace, 16) ||
       misaligned(cu_q, 4) || misaligned(cu_k, 4) || misaligned(out_lse, 4))
     return SPEC_ERR_ALIGN;
-  if (workspace_bytes < workspace_size()) return SPEC_ERR_WORKSPACE;
+  if (workspace_bytes < spec_prompt_attention_workspace_bytes(dims)) return SPEC_ERR_WORKSPACE;
   sv::DeviceInfo dev;
   const int st = sv::current_device(dev);
   if (st != SPEC_OK) return static_cast<spec_status>(st);
@@ -286,17 +1309,23 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
   a.len_k = cu_k ? cu_k : cu_q;
   a.out = out;
   a.lse = out_lse;
-  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
   a.B = dims.B;
   a.heads = dims.heads;
   a.kv_heads = dims.kv_heads;
+  a.G = dims.heads / dims.kv_heads;
   a.total_q = dims.total_q;
   a.total_k = dims.total_k;
-  a.q_stride = dims.q_stride;
   a.k_stride = dims.k_stride;
   a.v_stride = dims.v_stride;
-  a.ctrl = static_cast<int*>(workspace);
-  return launch<false>(a, dims.head_dim, dims.dtype, dims.total_q, reinterpret_cast<cudaStream_t>(stream));
+  a.tile_tokens = kBlock / a.G;
+  CUtensorMap maps[3];
+  if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, dims.total_q, dims.q_stride, a.G,
+                     a.tile_tokens) ||
+      !encode_tokens(&maps[1], dims.dtype, k, dims.head_dim, dims.kv_heads, dims.total_k, dims.k_stride, 1, kBlock) ||
+      !encode_tokens(&maps[2], dims.dtype, v, dims.head_dim, dims.kv_heads, dims.total_k, dims.v_stride, 1, kBlock))
+    return SPEC_ERR_CUDA;
+  return launch<false>(a, maps, dims.head_dim, dims.dtype, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 spec_status spec_attention_read_error(void* workspace, int32_t* error_word, spec_stream_t stream) {
