@@ -56,8 +56,10 @@
 namespace {
 
 constexpr int kBlock = 128;          // keys per block, rows per tile
-constexpr int kThreads = 320;        // two softmax warpgroups, an MMA warp, a load warp
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftWarps = 16;       // two row tiles x two halves of the 128 score columns x 4 warps of 32 rows
+constexpr int kThreads = 640;        // softmax warps, an MMA warp, load warps
+constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kCopyWarps = 2;        // load warps of the cache form
 constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
 constexpr int kItemUnits = 2;        // an item's start and end, in blocks
 constexpr int kMaxTree = 256;
@@ -66,9 +68,30 @@ constexpr int kJoinSplit = 4;        // CTAs that share the rows of one join
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // log2 of the largest weight before O is rescaled
 
+// a / b for non-negative values, in 32 bits where they fit (most do; the 64-bit division takes several hundred clocks).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The units before CTA c's share: `q` each, the first `r` CTAs one more.
+struct Shares {
+  long long q;
+  int r;
+  __device__ __forceinline__ long long before(int c) const { return q * c + min(c, r); }
+};
+
+__device__ __forceinline__ Shares shares_of(long long total, int grid) {
+  Shares s;
+  s.q = quot(total, grid);
+  s.r = static_cast<int>(total - s.q * grid);
+  return s;
+}
+
 // What a join needs to know of an item that was cut (one record per CTA).
 struct Cut {
-  long long start, total;  // first unit of the item, units in all
+  long long start;         // first unit of the item
+  Shares shares;
   int active;
   int b, kvh, tile, n;     // the item and its blocks
   int first;               // the CTA that holds block 0
@@ -151,17 +174,19 @@ __device__ long long floor_sum(long long n, long long m, long long x, long long 
   long long sum = 0;
   while (n > 0) {
     if (x >= m) {
-      sum += (n - 1) * n / 2 * (x / m);
-      x %= m;
+      const long long k = quot(x, m);
+      sum += (n - 1) * n / 2 * k;
+      x -= k * m;
     }
     if (y >= m) {
-      sum += n * (y / m);
-      y %= m;
+      const long long k = quot(y, m);
+      sum += n * k;
+      y -= k * m;
     }
     const long long top = x * n + y;
     if (top < m) break;
-    n = top / m;
-    y = top % m;
+    n = quot(top, m);
+    y = top - n * m;
     const long long t = m;
     m = x;
     x = t;
@@ -190,11 +215,6 @@ struct Cursor {
   long long start;  // first unit of the item
   Seq s;
 
-  __device__ void load(const AttnArgs& a) {
-    int err;
-    s = get_seq<kPaged>(a, b, err);
-    n = item_blocks<kPaged>(a, s, tile);
-  }
   __device__ void next(const AttnArgs& a) {
     start += n + kItemUnits;
     if (++tile < s.tiles) {
@@ -214,49 +234,80 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ long long share(long long total, long long cta, long long grid) {
-  return total * cta / grid;
-}
-
 template <int D, bool kPaged>
 struct Shape {
   static constexpr int kTileBytes = kBlock * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : (kPaged ? 8 : 8);
+  static constexpr int kStages = D == 64 ? 8 : (kPaged ? 5 : 4);
   static constexpr int kQBytes = kTiles<kPaged> * kTileBytes;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 256;  // O accumulators behind the two score tiles
 };
 
 struct Sync {
-  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], joint[3];
+  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], done;
   uint32_t tmem;
   int abort;
   int o_set[2];             // the softmax warps have written O themselves
-  unsigned spoiled[2][2][4];
-  long long u0, u1, total, start;
+  unsigned spoiled[2][4][4];
+  long long u0, u1, start;
+  Shares shares;
   int b, kvh, tile;
+  Seq seq;
   long long scan[kThreads / 32];
 };
 
-struct PagedShared {
-  float2 ml[2][2][kBlock];        // [segment parity][warpgroup][row] (reference, sum)
-  unsigned anc[2][kBlock][9];     // [warpgroup][row] ancestors of the row's node
+struct Exchange {
+  float top[2][2][kBlock];        // [tile][half][row] maxima of a block
+  float ref[2][2][kBlock];        // [segment parity][tile][row]
+  float sum[2][2][2][kBlock];     // [segment parity][tile][half][row]
+};
+
+struct TreeShared {
+  unsigned anc[2][kBlock][9];     // [tile][row] ancestors of the row's node
 };
 
 // A wait that gives up after kWaitLimitNs, or as soon as another warp has.
-__device__ __forceinline__ bool await(Sync& sh, uint64_t* bar, uint32_t parity) {
-  if (sv::mbar_try_wait(bar, parity)) return true;
+// The CTA then runs on to its end without waiting (its results are void, the
+// error word says so), so that no barrier is left with a warp missing.
+__device__ __forceinline__ void await(Sync& sh, uint64_t* bar, uint32_t parity) {
+  if (sv::mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = sv::global_timer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
-      if (sv::mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
-    if (sv::global_timer_ns() - t0 > sv::kWaitLimitNs) {
-      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-      return false;
-    }
+      if (sv::mbar_try_wait(bar, parity)) return;
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) return;
+    if (sv::global_timer_ns() - t0 > sv::kWaitLimitNs) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
   }
+}
+
+__device__ __forceinline__ bool aborted(Sync& sh) { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; }
+
+// Named barriers of the softmax warps: 1 + t the 256 threads of a row tile,
+// 3 those of both.
+__device__ __forceinline__ void meet(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool meet_any(int id, int threads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
+}
+
+// 16 bytes global -> shared, zeros where `bytes` is 0 (the address is not read then).
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// One arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sv::smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -344,7 +395,7 @@ template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
-  // (cache: map_k is the pool's, map_v the staged entries')
+  // (map_k and map_v: prompts only)
   using Sh = Shape<D, kPaged>;
   constexpr int kNT = kTiles<kPaged>;
   extern __shared__ uint8_t raw[];
@@ -353,27 +404,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + Sh::kQBytes;
   uint8_t* tail = ring + Sh::kStages * Sh::kTileBytes;
   Sync& sh = *reinterpret_cast<Sync*>(tail);
-  PagedShared& ps = *reinterpret_cast<PagedShared*>(tail + (sizeof(Sync) + 15) / 16 * 16);  // (cache only)
+  Exchange& ex = *reinterpret_cast<Exchange*>(tail + (sizeof(Sync) + 15) / 16 * 16);
+  TreeShared& ts = *reinterpret_cast<TreeShared*>(&ex + 1);  // (cache only)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  const long long grid = gridDim.x;
+  const int grid = gridDim.x;
 
   sv::griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      sv::mbar_init(&sh.full[i], 1);
+      sv::mbar_init(&sh.full[i], kPaged ? 32 * kCopyWarps : 1);
       sv::mbar_init(&sh.empty[i], 1);
     }
     sv::mbar_init(&sh.q_full, 1);
     sv::mbar_init(&sh.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       sv::mbar_init(&sh.s_full[t], 1);
-      sv::mbar_init(&sh.p_full[t], 4);
+      sv::mbar_init(&sh.p_full[t], 8);
       sv::mbar_init(&sh.o_full[t], 1);
-      sv::mbar_init(&sh.o_free[t], kPaged ? 8 : 4);
-      sv::mbar_init(&sh.joint[1 + t], 4);
+      sv::mbar_init(&sh.o_free[t], kPaged ? 16 : 8);
     }
-    sv::mbar_init(&sh.joint[0], 8);
+    sv::mbar_init(&sh.done, 1);
     sv::fence_barrier_init();
     sh.abort = 0;
     a.cuts[cta].active = 0;
@@ -384,8 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kLoadWarp && lane == 0) {
     sv::prefetch_tensor_map(&map_q);
-    sv::prefetch_tensor_map(&map_k);
-    sv::prefetch_tensor_map(&map_v);
+    if (!kPaged) {
+      sv::prefetch_tensor_map(&map_k);
+      sv::prefetch_tensor_map(&map_v);
+    }
   }
 
   // ---- this CTA's share of the units: a scan over the sequences
@@ -423,12 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pass == 0 && b0 + kThreads < a.B) continue;  // the total is not known yet
       if (pass == 0) total = seen;
       if (pass == 0 && a.B > kThreads) break;          // find the start in a second pass
-      const long long u0 = share(total, cta, grid);
+      const long long u0 = shares_of(total, grid).before(cta);
       if (units > 0 && before <= u0 && u0 < before + units) {
-        const long long per_head = units / a.kv_heads, r = (u0 - before) % per_head;
+        const long long per_head = quot(units, a.kv_heads), kvh = quot(u0 - before, per_head);
+        const long long r = u0 - before - kvh * per_head;
         int lo = 0, hi = s.tiles;  // the last tile that starts at or before r
         if (kPaged) {
-          lo = static_cast<int>(r / (item_blocks<kPaged>(a, s, 0) + kItemUnits));
+          lo = static_cast<int>(quot(r, item_blocks<kPaged>(a, s, 0) + kItemUnits));
         } else {
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -437,17 +491,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         sh.b = b;
-        sh.kvh = static_cast<int>((u0 - before) / per_head);
+        sh.kvh = static_cast<int>(kvh);
         sh.tile = lo;
+        sh.seq = s;
         sh.start = u0 - r + (lo ? head_units<kPaged>(a, s, lo) : 0);
       }
     }
     if (a.B <= kThreads) break;
   }
   if (tid == 0) {
-    sh.u0 = share(total, cta, grid);
-    sh.u1 = share(total, cta + 1, grid);
-    sh.total = total;
+    sh.shares = shares_of(total, grid);
+    sh.u0 = sh.shares.before(cta);
+    sh.u1 = sh.shares.before(cta + 1);
   }
   if (kPaged && a.parents) {  // trees are checked once per sequence
     for (int b = cta; b < a.B; b += gridDim.x) {
@@ -472,117 +527,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     at.kvh = sh.kvh;
     at.tile = sh.tile;
     at.start = sh.start;
-    at.load(a);
+    at.s = sh.seq;
+    at.n = item_blocks<kPaged>(a, at.s, at.tile);
   }
-  bool ok = true;
 
-  if (warp == kLoadWarp) {
+  if (warp >= kLoadWarp) {
     // ------------------------------------------------------------- loads
     uint32_t loads = 0, segs = 0;
     const uint64_t keep = sv::l2_policy_evict_last(), once = sv::l2_policy_evict_first();
-    const uint64_t policy = kPaged && a.S * a.G <= kBlock ? once : keep;
-    // takes the next slot of the ring (all lanes; lane 0 waits and announces the bytes)
-    auto slot_of = [&]() -> uint8_t* {
-      const uint32_t slot = loads % Sh::kStages;
-      if (lane == 0) {
-        ok = ok && await(sh, &sh.empty[slot], (loads / Sh::kStages & 1) ^ 1);
-        if (ok) sv::mbar_arrive_expect_tx(&sh.full[slot], Sh::kTileBytes);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      return ring + slot * Sh::kTileBytes;
+    const int lw = warp - kLoadWarp;
+    auto load_q = [&]() {  // by one thread
+      if (segs > 0) await(sh, &sh.q_empty, (segs - 1) & 1);
+      if (aborted(sh)) return;
+      const int tok = at.s.q0 + at.tile * a.tile_tokens * kNT;
+      sv::mbar_arrive_expect_tx(&sh.q_full, kNT * a.tile_tokens * a.G * D * 2);
+      for (int t = 0; t < kNT; ++t)
+        for (int h = 0; h < D / 64; ++h)
+          sv::tma_load_3d(q_tile + t * Sh::kTileBytes + h * (kBlock * 128), &map_q, &sh.q_full, h * 64, at.kvh * a.G,
+                          tok + t * a.tile_tokens, once);
     };
-    auto bar_of = [&]() { return &sh.full[loads % Sh::kStages]; };
-    for (; ok && at.start < u1; at.next(a)) {
-      const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
-      const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
-      if (hi <= lo) continue;
-      auto load_q = [&]() {
-        if (lane == 0 && ok) {
-          ok = segs == 0 || await(sh, &sh.q_empty, (segs - 1) & 1);
-          if (ok) {
-            const int tok = at.s.q0 + at.tile * a.tile_tokens * kNT;
-            sv::mbar_arrive_expect_tx(&sh.q_full, kNT * a.tile_tokens * a.G * D * 2);
-            for (int t = 0; t < kNT; ++t)
-              for (int h = 0; h < D / 64; ++h)
-                sv::tma_load_3d(q_tile + t * Sh::kTileBytes + h * (kBlock * 128), &map_q, &sh.q_full, h * 64,
-                                at.kvh * a.G, tok + t * a.tile_tokens, once);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      };
-      if (kPaged) {
-        const int committed = a.staged ? blocks_of(at.s.base) : at.n;  // blocks read from the pool
-        const int limit = a.staged ? at.s.base : at.s.base + at.s.Lq;
-        const int* table = a.bt + static_cast<long long>(at.b) * a.max_pages;
-        const int x_k = at.kvh * D, x_v = (a.kv_heads + at.kvh) * D;
-        int r0[4], r1[4];  // this lane's four rows of the block before, of this block
-        auto rows_of = [&](int j, int (&r)[4]) {
-          if (j >= committed) {
-            const int i0 = (j - committed) * kBlock + 4 * lane;
+    if (lw < (kPaged ? kCopyWarps : 1)) {
+      for (; at.start < u1; at.next(a)) {
+        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
+        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+        if (hi <= lo) continue;
+        if (kPaged) {
+          const int committed = a.staged ? blocks_of(at.s.base) : at.n;  // blocks read from the pool
+          const int limit = a.staged ? at.s.base : at.s.base + at.s.Lq;
+          const int* table = a.bt + static_cast<long long>(at.b) * a.max_pages;
+          const long long entry = 4ll * a.kv_heads * D;  // bytes
+          constexpr int kRows = kBlock / kCopyWarps;     // rows of a tile this warp copies
+          constexpr int kEach = kRows / 32;              // rows a lane looks up: lane, lane + 32, ..
+          constexpr int kChunks = D / 8;                 // 16-byte pieces of a row
+          constexpr int kAtOnce = 32 / kChunks;          // rows one instruction copies
+          const int chunk = lane % kChunks, sub = lane / kChunks;
+          int r0[kEach], r1[kEach] = {};  // rows of the block before, of this block; -1: zeros
+          auto rows_of = [&](int j, int (&r)[kEach]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = i0 + e < at.s.Lq ? at.b * a.S + i0 + e : a.B * a.S;
-            return;
-          }
-          const int p0 = j * kBlock + 4 * lane;
-          int col = p0 / a.page_size, slot = p0 - col * a.page_size;
-          bool bad = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            r[e] = a.num_pages * a.page_size;
-            if (p0 + e < limit) {
-              const int page = table[col];
-              if (page >= 0 && page < a.num_pages) r[e] = page * a.page_size + slot;
-              else bad = true;
+            for (int e = 0; e < kEach; ++e) {
+              const int in = lw * kRows + 32 * e + lane;
+              r[e] = -1;
+              if (j >= committed) {
+                const int i = (j - committed) * kBlock + in;
+                if (i < at.s.Lq) r[e] = at.b * a.S + i;
+              } else if (j * kBlock + in < limit) {
+                const int p = j * kBlock + in, col = p / a.page_size;
+                const int page = table[col];
+                if (page >= 0 && page < a.num_pages) r[e] = page * a.page_size + (p - col * a.page_size);
+                else atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
+              }
             }
-            if (++slot == a.page_size) {
-              slot = 0;
-              ++col;
-            }
-          }
-          if (bad) atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
-        };
-        auto gather = [&](int j, const int (&r)[4], int x) {
-          uint8_t* dst = slot_of();
-          if (!ok) return;
-          const CUtensorMap* map = j >= committed ? &map_v : &map_k;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            sv::tma_gather4(dst + h * (kBlock * 128) + lane * 512, map, bar_of(), x + h * 64, r[0], r[1], r[2], r[3],
-                            policy);
-          ++loads;
-        };
-        rows_of(lo, r0);
-        gather(lo, r0, x_k);
-        load_q();
-        for (int j = lo; ok && j < hi; ++j) {
-          if (j + 1 < hi) {
-            rows_of(j + 1, r1);
-            gather(j + 1, r1, x_k);
-          }
-          if (ok) gather(j, r0, x_v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r0[e] = r1[e];
-        }
-      } else {
-        for (int j = lo; ok && j < hi; ++j) {
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            uint8_t* dst = slot_of();
-            if (ok && lane == 0)
-              for (int h = 0; h < D / 64; ++h)
-                sv::tma_load_3d(dst + h * (kBlock * 128), kv ? &map_v : &map_k, bar_of(), h * 64, at.kvh,
-                                static_cast<int>(at.s.k0) + j * kBlock, policy);
+          };
+          auto copy = [&](int j, const int (&r)[kEach], int head) {
+            const uint32_t slot = loads % Sh::kStages;
+            await(sh, &sh.empty[slot], (loads / Sh::kStages & 1) ^ 1);
             ++loads;
-            if (j == lo && kv == 0) load_q();
+            if (aborted(sh)) return;
+            const char* from = static_cast<const char*>(j >= committed ? a.staged : a.k) + head * (D * 2) + chunk * 16;
+            const uint32_t to = sv::smem_u32(ring + slot * Sh::kTileBytes) + (chunk >> 3) * (kBlock * 128);
+#pragma unroll
+            for (int i = 0; i < kRows / kAtOnce; ++i) {
+              const int in = i * kAtOnce + sub;                   // row within this warp's
+              const int e = i * kAtOnce / 32;                     // (the same for the whole warp)
+              const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
+              const int spot = lw * kRows + in;
+              copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + (row < 0 ? 0 : row * entry),
+                      row < 0 ? 0 : 16);
+            }
+            copies_arrive(&sh.full[slot]);
+          };
+          rows_of(lo, r0);
+          copy(lo, r0, at.kvh);
+          if (lw == 0 && lane == 0) load_q();
+          __syncwarp();
+          for (int j = lo; j < hi; ++j) {
+            if (j + 1 < hi) {
+              rows_of(j + 1, r1);
+              copy(j + 1, r1, at.kvh);
+            }
+            copy(j, r0, a.kv_heads + at.kvh);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) r0[e] = r1[e];
+          }
+        } else if (lane == 0) {
+          for (int j = lo; j < hi; ++j) {
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t slot = loads % Sh::kStages;
+              await(sh, &sh.empty[slot], (loads / Sh::kStages & 1) ^ 1);
+              if (!aborted(sh)) {
+                sv::mbar_arrive_expect_tx(&sh.full[slot], Sh::kTileBytes);
+                for (int h = 0; h < D / 64; ++h)
+                  sv::tma_load_3d(ring + slot * Sh::kTileBytes + h * (kBlock * 128), kv ? &map_v : &map_k,
+                                  &sh.full[slot], h * 64, at.kvh, static_cast<int>(at.s.k0) + j * kBlock, keep);
+              }
+              ++loads;
+              if (j == lo && kv == 0) load_q();
+            }
           }
         }
+        ++segs;
       }
-      ++segs;
-    }
-    if (!ok) {  // leave no copy in flight
-      if (lane == 0) {
-        const uint32_t first = loads > Sh::kStages ? loads - Sh::kStages : 0;
-        for (uint32_t i = first; i < loads; ++i) sv::mbar_wait(&sh.full[i % Sh::kStages], i / Sh::kStages & 1);
+      if (kPaged) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
+      if (aborted(sh) && lane == 0) {  // leave no copy in flight
+        if (!kPaged) {
+          const uint32_t first = loads > Sh::kStages ? loads - Sh::kStages : 0;
+          for (uint32_t i = first; i < loads; ++i) sv::mbar_wait(&sh.full[i % Sh::kStages], i / Sh::kStages & 1);
+        }
+        if (lw == 0 && segs > 0) sv::mbar_wait(&sh.q_full, (segs - 1) & 1);
+      }
+      __syncwarp();
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMA
@@ -592,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ring_addr = sv::smem_u32(ring), q_addr = sv::smem_u32(q_tile);
       auto arrived = [&]() -> uint32_t {  // waits for the next load; its address
         const uint32_t slot = loads % Sh::kStages;
-        ok = ok && await(sh, &sh.full[slot], loads / Sh::kStages & 1);
+        await(sh, &sh.full[slot], loads / Sh::kStages & 1);
+        if (kPaged) sv::fence_proxy_async_smem();  // the copies wrote through the generic proxy
         sv::tc_fence_after_sync();
         return ring_addr + slot * Sh::kTileBytes;
       };
@@ -608,42 +664,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // P V of one block; waits for P and, first, for O to be free
       auto values = [&](int t, uint32_t v_addr, bool first) {
-        if (first && used[t] > 0) ok = ok && await(sh, &sh.o_free[t], (used[t] - 1) & 1);
-        ok = ok && await(sh, &sh.p_full[t], p_cnt[t] & 1);
+        if (first && used[t] > 0) await(sh, &sh.o_free[t], (used[t] - 1) & 1);
+        await(sh, &sh.p_full[t], p_cnt[t] & 1);
         ++p_cnt[t];
-        if (!ok) return;
         sv::tc_fence_after_sync();
         const bool fresh = first && !*reinterpret_cast<volatile int*>(&sh.o_set[t]);
 #pragma unroll
         for (int k = 0; k < kBlock / 16; ++k)
-          sv::mma_f16_ts(tmem + Sh::kO + t * D, tmem + t * kBlock + k * 8,
+          sv::mma_f16_ts(tmem + Sh::kO + t * D, tmem + t * kBlock + (k & 3) * 8 + (k >> 2) * 64,
                          sv::smem_desc_mn_sw128(v_addr + k * 2048, kBlock * 128), kIdO, !(fresh && k == 0));
       };
-      for (; ok && at.start < u1; at.next(a)) {
+      for (; at.start < u1; at.next(a)) {
         const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
         const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
         const int nb = hi - lo;
         if (nb <= 0) continue;
-        ok = ok && await(sh, &sh.q_full, segs & 1);
+        await(sh, &sh.q_full, segs & 1);
         if (kPaged) {
-          for (int i = 0; i < 2 && i < nb && ok; ++i) {
+          for (int i = 0; i < 2 && i < nb; ++i) {
             const uint32_t k_addr = arrived();
-            if (!ok) break;
             scores(i, k_addr);
             sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
           }
           if (nb <= 2) sv::mma_commit(&sh.q_empty);
-          for (int i = 0; ok && i < nb; ++i) {
+          for (int i = 0; i < nb; ++i) {
             const int t = i & 1;
             const uint32_t v_addr = arrived();
-            if (ok) values(t, v_addr, i < 2);
-            if (!ok) break;
+            values(t, v_addr, i < 2);
             sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
             if (i + 2 >= nb) sv::mma_commit(&sh.o_full[t]);
             if (i + 2 < nb) {
               const uint32_t k_addr = arrived();
-              if (!ok) break;
-              scores(t, k_addr);
+                scores(t, k_addr);
               sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
               if (i + 3 == nb) sv::mma_commit(&sh.q_empty);
             }
@@ -653,28 +705,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const bool two = at.s.Lq - at.tile * a.tile_tokens * 2 > a.tile_tokens;
           uint32_t k_addr = arrived();
-          if (ok) {
-            scores(0, k_addr);
-            if (two) scores(1, k_addr);
-            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
-            if (nb == 1) sv::mma_commit(&sh.q_empty);
-          }
-          for (int i = 0; ok && i < nb; ++i) {
+          scores(0, k_addr);
+          if (two) scores(1, k_addr);
+          sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+          if (nb == 1) sv::mma_commit(&sh.q_empty);
+          for (int i = 0; i < nb; ++i) {
             const uint32_t v_addr = arrived(), v_slot = loads++ % Sh::kStages;
-            if (ok) values(0, v_addr, i == 0);
-            if (!ok) break;
+            values(0, v_addr, i == 0);
             if (i + 1 == nb) sv::mma_commit(&sh.o_full[0]);
             uint32_t k_slot = 0;
             if (i + 1 < nb) {
               k_addr = arrived();
               k_slot = loads++ % Sh::kStages;
-              if (!ok) break;
-              scores(0, k_addr);
+                scores(0, k_addr);
             }
             if (two) {
               values(1, v_addr, i == 0);
-              if (!ok) break;
-            }
+              }
             sv::mma_commit(&sh.empty[v_slot]);
             if (two && i + 1 == nb) sv::mma_commit(&sh.o_full[1]);
             if (i + 1 < nb) {
@@ -688,25 +735,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++segs;
       }
+      if (aborted(sh)) {  // the products in flight end before the tensor memory is given back
+        sv::mma_commit(&sh.done);
+        sv::mbar_wait(&sh.done, 0);
+      }
     }
     __syncwarp();
-  } else if (warp < kMmaWarp) {
+  } else {
     // ----------------------------------------------------------- softmax
-    const int t = warp >> 2, row = tid & (kBlock - 1);
+    // thread: row `row` of tile t, score columns 64 half .. + 63
+    const int t = warp >> 3, half = (warp >> 2) & 1, row = tid & (kBlock - 1);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_addr = tmem + t * kBlock + lanes;
+    const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
     const float c2 = a.scale_log2;
-    uint32_t loads = 0, s_cnt = 0, used[2] = {0, 0}, j_cnt[3] = {0, 0, 0}, merges = 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {  // one answer for the whole warp
-      ok = __all_sync(0xffffffffu, ok && await(sh, bar, parity));
-    };
-    auto meet = [&](int g) {  // all warps of a group (0: both warpgroups, 1 + t: this one)
+    uint32_t loads = 0, s_cnt = 0, used[2] = {0, 0}, merges = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      await(sh, bar, parity);
       __syncwarp();
-      if (lane == 0) sv::mbar_arrive(&sh.joint[g]);
-      wait(&sh.joint[g], j_cnt[g] & 1);
-      ++j_cnt[g];
     };
-    for (; ok && at.start < u1; at.next(a)) {
+    for (; at.start < u1; at.next(a)) {
       const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
       const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
       const int nb = hi - lo;
@@ -716,44 +764,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok0 = item_tok + (kPaged ? 0 : t * a.tile_tokens);
       const int rows = max(0, min(a.tile_tokens, s.Lq - tok0)) * a.G;
       const bool both = kPaged ? nb > 1 : s.Lq - item_tok > a.tile_tokens;  // the second score tile is in use
-      if (t == 0 && row == 0 && lo > 0) {
+      if (tid == 0 && lo > 0) {
         Cut cut;
         cut.start = at.start;
-        cut.total = sh.total;
+        cut.shares = sh.shares;
         cut.b = at.b;
         cut.kvh = at.kvh;
         cut.tile = at.tile;
         cut.n = at.n;
-        int p = cta - 1;
-        while (share(cut.total, p, grid) == u0) --p;  // (CTAs without a share)
-        cut.first = p;
-        cut.active = share(cut.total, p, grid) - at.start - kItemUnits <= 0;
+        cut.first = cta - 1;  // (every CTA before one with a share has one)
+        cut.active = sh.shares.before(cta - 1) - at.start - kItemUnits <= 0;
         a.cuts[cta] = cut;
       }
       if (t == 1 && !both) {
         loads += 2 * nb;
         ++used[0];
+        ++merges;
         continue;
       }
       const bool alive = (row & ~31) < rows;  // the warp has a row
       const int i_tok = tok0 + row / a.G;     // this row's token
       const int committed = kPaged && a.staged ? blocks_of(s.base) : at.n;
       const bool tree = kPaged && a.parents != nullptr;
-      if (tree && alive) {
-        unsigned* anc = ps.anc[t][row];
+      if (tree) {
+        meet(1 + t, 256);  // the last segment's readers are done
+        if (half == 0 && alive) {
+          unsigned* anc = ts.anc[t][row];
 #pragma unroll
-        for (int w = 0; w < 8; ++w) anc[w] = 0;
-        int p = min(i_tok, s.Lq - 1);
-        while (p >= 0) {
-          anc[p >> 5] |= 1u << (p & 31);
-          const int up = a.parents[static_cast<long long>(at.b) * a.S + p];
-          p = up < p ? up : -1;  // (a bad parent is flagged; the walk still ends)
+          for (int w = 0; w < 8; ++w) anc[w] = 0;
+          int p = min(i_tok, s.Lq - 1);
+          while (p >= 0) {
+            anc[p >> 5] |= 1u << (p & 31);
+            const int up = a.parents[static_cast<long long>(at.b) * a.S + p];
+            p = up < p ? up : -1;  // (a bad parent is flagged; the walk still ends)
+          }
         }
+        meet(1 + t, 256);
       }
-      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of its weights
+      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of this half's weights
       float top = -INFINITY;             // the same reference as a score
 
-      for (int i = kPaged ? t : 0; ok && i < nb; i += kPaged ? 2 : 1) {
+      for (int i = kPaged ? t : 0; i < nb; i += kPaged ? 2 : 1) {
         const bool first = i < (kPaged ? 2 : 1);
         const int j = lo + i;
         // the block's first position (fresh: index among the new entries), how far this row and the item's first
@@ -772,43 +823,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool look = masked && (!kPaged || (s.Lq > 1 && (fresh || !a.staged)));
         wait(&sh.s_full[t], s_cnt & 1);
         ++s_cnt;
-        if (!ok) break;
         sv::tc_fence_after_sync();
         unsigned spoil[4] = {0, 0, 0, 0};
         if (look) {
+          // the V tile's rows (one per thread of a half), each thread a share of the columns
           const bool pair = !kPaged && both;
-          const int g = pair ? 0 : 1 + t, part = pair ? t : 0, box = pair ? 0 : t;
+          const int parts = pair ? 4 : 2, part = pair ? 2 * t + half : half, box = pair ? 0 : t;
+          const int bar = pair ? 3 : 1 + t, crowd = pair ? 512 : 256;
           const uint32_t rank = loads + v_rank<kPaged>(i, nb), slot = rank % Sh::kStages;
           wait(&sh.full[slot], rank / Sh::kStages & 1);
           uint8_t* vrow = ring + slot * Sh::kTileBytes + row * 128;
-          const int chunks = pair ? D / 16 : D / 8, c0 = part * chunks;
+          const int chunks = D / 8 / parts, c0 = part * chunks;
           bool odd = false;
-          if (ok)
-            for (int c = 0; c < chunks; ++c) {
-              const int cc = c0 + c;
-              const uint4 w = *reinterpret_cast<const uint4*>(vrow + (cc >> 3) * (kBlock * 128) +
-                                                              (((cc & 7) ^ (row & 7)) << 4));
-              odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
-            }
+          for (int c = c0; c < c0 + chunks; ++c) {
+            const uint4 w =
+                *reinterpret_cast<const uint4*>(vrow + (c >> 3) * (kBlock * 128) + (((c & 7) ^ (row & 7)) << 4));
+            odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
+          }
           const unsigned word = __ballot_sync(0xffffffffu, odd);
           if (lane == 0) sh.spoiled[box][part][warp & 3] = word;
-          meet(g);
-          if (!ok) break;
+          meet(bar, crowd);
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            spoil[w] = *reinterpret_cast<volatile unsigned*>(&sh.spoiled[box][0][w]) |
-                       (pair ? *reinterpret_cast<volatile unsigned*>(&sh.spoiled[box][1][w]) : 0u);
-          const unsigned own = (warp & 2) ? ((warp & 1) ? spoil[3] : spoil[2]) : ((warp & 1) ? spoil[1] : spoil[0]);
+            for (int k = 0; k < parts; ++k) spoil[w] |= *reinterpret_cast<volatile unsigned*>(&sh.spoiled[box][k][w]);
+          const unsigned own =
+              (warp & 2) ? ((warp & 1) ? spoil[3] : spoil[2]) : ((warp & 1) ? spoil[1] : spoil[0]);
           if (own >> lane & 1u) {
-            for (int c = 0; c < chunks; ++c) {
-              const int cc = c0 + c;
-              *reinterpret_cast<uint4*>(vrow + (cc >> 3) * (kBlock * 128) + (((cc & 7) ^ (row & 7)) << 4)) =
+            for (int c = c0; c < c0 + chunks; ++c)
+              *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kBlock * 128) + (((c & 7) ^ (row & 7)) << 4)) =
                   make_uint4(0, 0, 0, 0);
-            }
             sv::fence_proxy_async_smem();
           }
-          meet(g);
-          if (!ok) break;
+          meet(bar, crowd);
           if (!kPaged) {  // keys behind the sequence's are other sequences': zeroed, not added
             const int keys = s.base + s.Lq - pos0;
 #pragma unroll
@@ -817,121 +863,119 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const bool spoils = (spoil[0] | spoil[1] | spoil[2] | spoil[3]) != 0;
-        if (first && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
-        if (alive) {
-          unsigned word[4];
-          if (masked) {
-            if (tree && (fresh || !a.staged)) {
-              const unsigned* anc = ps.anc[t][row];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                // bits idx0 .. idx0 + 31 of the ancestors; everything before the new entries is seen
-                const int idx0 = pos0 + 32 * w - (fresh && a.staged ? 0 : s.base);
-                const int k = idx0 >> 5, shift = idx0 & 31;
-                const unsigned b0 = k < 0 ? 0xffffffffu : (k < 8 ? anc[k] : 0u);
-                const unsigned b1 = k + 1 < 0 ? 0xffffffffu : (k + 1 < 8 ? anc[k + 1] : 0u);
-                word[w] = __funnelshift_r(b0, b1, shift);
-              }
-            } else {
-#pragma unroll
-              for (int w = 0; w < 4; ++w)
-                word[w] = seen >= 32 * (w + 1) ? 0xffffffffu : (seen <= 32 * w ? 0u : (1u << (seen - 32 * w)) - 1u);
-            }
+        if (first && half == 0 && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
+        // bit c of word w: column 32 w + c is seen
+        auto seen_word = [&](int w) -> unsigned {
+          if (tree && (fresh || !a.staged)) {
+            // bits idx0 .. idx0 + 31 of the ancestors; everything before the new entries is seen
+            const unsigned* anc = ts.anc[t][row];
+            const int idx0 = pos0 + 32 * w - (a.staged ? 0 : s.base), k = idx0 >> 5;
+            const unsigned b0 = k < 0 ? 0xffffffffu : (k < 8 ? anc[k] : 0u);
+            const unsigned b1 = k + 1 < 0 ? 0xffffffffu : (k + 1 < 8 ? anc[k + 1] : 0u);
+            return __funnelshift_r(b0, b1, idx0 & 31);
           }
-          // 64 scores, -infinity where the row must not see the key
-          auto scores = [&](int h, float (&x)[64]) {
-            sv::tmem_load_64(s_addr + 64 * h, x);
-            if (!masked) return;
+          return seen >= 32 * (w + 1) ? 0xffffffffu : (seen <= 32 * w ? 0u : (1u << (seen - 32 * w)) - 1u);
+        };
+        auto read = [&](int h, float (&x)[32]) {  // 32 scores, -infinity where the row must not see the key
+          sv::tmem_load_32(s_addr + 64 * half + 32 * h, x);
+          if (!masked) return;
+          const unsigned m = seen_word(2 * half + h);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(word[2 * h + (c >> 5)] >> (c & 31) & 1u)) x[c] = -INFINITY;
-          };
-          float blk = -INFINITY;
+          for (int c = 0; c < 32; ++c)
+            if (!(m >> c & 1u)) x[c] = -INFINITY;
+        };
+        bool raise = false;
+        float blk = -INFINITY;
+        if (alive) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x[64];
-            scores(h, x);
+            float x[32];
+            read(h, x);
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+            for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
             blk = fmaxf(blk, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           }
           // raise the reference where a weight would exceed 2^kSlack
-          const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
-          const float was = ref;
-          if (raise) {
-            top = blk;
-            ref = top * c2;
-          }
-          const bool lift = !first && __any_sync(0xffffffffu, raise);
-          const float off = ref == -INFINITY ? 0.f : -ref;
-          if (lift) {
-            const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
-            sum *= f;
-            const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              sv::tmem_load_32(o_addr + c, o);
-              uint32_t w[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-              sv::tmem_store_32(o_addr + c, w);
+          raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+        }
+        if (meet_any(1 + t, 256, raise || spoils)) {
+          ex.top[t][half][row] = blk;
+          meet(1 + t, 256);
+          if (alive) {
+            blk = fmaxf(blk, ex.top[t][half ^ 1][row]);
+            raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+            const float was = ref;
+            if (raise) {
+              top = blk;
+              ref = top * c2;
             }
-            sv::tmem_wait_st();
-          }
-          if (spoils) {  // rare: values that are infinite or not a number, for the rows that see them
-            const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
-            if (first) {
-              if (used[t] > 0) wait(&sh.o_free[t], (used[t] - 1) & 1);
-              sv::tc_fence_after_sync();
-              uint32_t w[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = 0;
-              for (int c = 0; c < D; c += 32) sv::tmem_store_32(o_addr + c, w);
-              sv::tmem_wait_st();
-            }
+            if (!first && __any_sync(0xffffffffu, raise)) {
+              const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
+              sum *= f;
 #pragma unroll 1
-            for (int c = 0; c < kBlock; ++c) {
-              const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
-              if (!(sw >> (c & 31) & 1u)) continue;
-              const unsigned vw = c < 64 ? (c < 32 ? word[0] : word[1]) : (c < 96 ? word[2] : word[3]);
-              const bool mine = vw >> (c & 31) & 1u;
-              const float sc = sv::tmem_load_1(s_addr + c);
-              const float p = exp2_approx(fmaf(sc, c2, off));
-              const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
-#pragma unroll 1
-              for (int d = 0; d < D; d += 32) {
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                 float o[32];
-                sv::tmem_load_32(o_addr + d, o);
+                sv::tmem_load_32(o_addr + c, o);
                 uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  w[e] = __float_as_uint(mine && v != nullptr ? o[e] + p * to_f(v[d + e]) : o[e]);
-                sv::tmem_store_32(o_addr + d, w);
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                sv::tmem_store_32(o_addr + c, w);
+              }
+              sv::tmem_wait_st();
+            }
+            if (spoils) {  // rare: values that are infinite or not a number, for the rows that see them
+              const float off = ref == -INFINITY ? 0.f : -ref;
+              if (first) {
+                if (used[t] > 0) wait(&sh.o_free[t], (used[t] - 1) & 1);
+                sv::tc_fence_after_sync();
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = 0;
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) sv::tmem_store_32(o_addr + c, w);
                 sv::tmem_wait_st();
+              }
+#pragma unroll 1
+              for (int c = 0; c < kBlock; ++c) {
+                const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
+                if (!(sw >> (c & 31) & 1u)) continue;
+                const bool mine = seen_word(c >> 5) >> (c & 31) & 1u;
+                const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c), c2, off));
+                const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
+#pragma unroll 1
+                for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                  float o[32];
+                  sv::tmem_load_32(o_addr + d, o);
+                  uint32_t w[32];
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    w[e] = __float_as_uint(mine && v != nullptr ? o[e] + p * to_f(v[d + e]) : o[e]);
+                  sv::tmem_store_32(o_addr + d, w);
+                  sv::tmem_wait_st();
+                }
               }
             }
           }
+          if (spoils) meet(1 + t, 256);  // either half has read the other's scores
+        }
+        if (alive) {
+          const float off = ref == -INFINITY ? 0.f : -ref;
           const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // the scores are read a second time rather than held: P's 32 columns of a half lie below the scores still
-          // to be read
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x[64];
-            scores(h, x);
-            uint32_t w[32];
+            float x[32];
+            read(h, x);  // again, rather than held meanwhile; the weights are written over scores read before
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int c = 2 * e;
-              float2 z = fma2(make_float2(x[c], x[c + 1]), cc, oo);
+            for (int e = 0; e < 16; ++e) {
+              float2 z = fma2(make_float2(x[2 * e], x[2 * e + 1]), cc, oo);
               z.x = exp2_approx(z.x);
               z.y = exp2_approx(z.y);
               acc[e & 1] = add2(acc[e & 1], z);
               w[e] = pack2(z.x, z.y, T());
             }
-            sv::tmem_store_32(s_addr + h * 32, w);
+            sv::tmem_store_16(s_addr + half * 64 + h * 16, w);
           }
           const float2 both_acc = add2(acc[0], acc[1]);
           sum += both_acc.x + both_acc.y;
@@ -942,57 +986,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) sv::mbar_arrive(&sh.p_full[t]);
       }
       loads += 2 * nb;
-      if (!ok) break;
 
       // ---- end of the segment: normalise and write, or leave partial rows
       const bool whole = lo == 0 && hi == at.n;
       const long long slot = (static_cast<long long>(cta) * 2 + (lo > 0 ? 0 : 1)) * (kNT * kBlock);
-      int d0 = 0, d1 = D;
-      float f0 = 1.f, f1 = 0.f, all = sum, base2 = ref;
-      if (kPaged) {
-        if (both) {
-          float2(&ml)[2][kBlock] = ps.ml[merges & 1];
-          ++merges;
-          ml[t][row] = make_float2(ref, sum);
-          meet(0);
-          if (!ok) break;
-          const float2 m0 = ml[0][row], m1 = ml[1][row];
-          base2 = fmaxf(m0.x, m1.x);
-          f0 = m0.x == -INFINITY ? 0.f : exp2_approx(m0.x - base2);
-          f1 = m1.x == -INFINITY ? 0.f : exp2_approx(m1.x - base2);
-          all = m0.y * f0 + m1.y * f1;
-          d0 = t * (D / 2);
-          d1 = d0 + D / 2;
-        }
-        wait(&sh.o_full[0], used[0] & 1);
-        if (both) wait(&sh.o_full[1], used[1] & 1);
-      } else {
-        wait(&sh.o_full[t], used[t] & 1);
+      const uint32_t par = merges++ & 1;
+      if (half == 0) ex.ref[par][t][row] = ref;
+      ex.sum[par][t][half][row] = sum;
+      // the warps that share the rows' columns: two, or in the cache form with both tiles in use four
+      const bool four = kPaged && both;
+      meet(four ? 3 : 1 + t, four ? 512 : 256);
+      const int t0 = kPaged ? 0 : t, width = four ? D / 4 : D / 2, d0 = (four ? 2 * t + half : half) * width;
+      float f0 = 1.f, f1 = 0.f, all = ex.sum[par][t0][0][row] + ex.sum[par][t0][1][row], base2 = ex.ref[par][t0][row];
+      if (four) {
+        const float m0 = base2, m1 = ex.ref[par][1][row];
+        base2 = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - base2);
+        f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - base2);
+        all = all * f0 + (ex.sum[par][1][0][row] + ex.sum[par][1][1][row]) * f1;
       }
-      if (!ok) break;
+      wait(&sh.o_full[t0], used[t0] & 1);
+      if (four) wait(&sh.o_full[1], used[1] & 1);
       sv::tc_fence_after_sync();
       if (alive) {
         const bool mine = row < rows;
         const long long orow = (static_cast<long long>(s.q0) + i_tok) * a.heads + at.kvh * a.G + row % a.G;
-        const float inv = whole ? (all == 0.f ? 0.f : 1.f / all) : 1.f;
         const bool none = all == 0.f;
+        const float inv = whole && !none ? 1.f / all : 1.f;
         const int prow = kPaged ? row : t * kBlock + row;
-        const uint32_t o_addr = tmem + Sh::kO + (kPaged ? 0 : t * D) + lanes;
+        const uint32_t from = tmem + Sh::kO + t0 * D + lanes;
 #pragma unroll 1
-        for (int d = d0; d < d1; d += 32) {
-          float o[32];
-          sv::tmem_load_32(o_addr + d, o);
-          if (kPaged && both) {
-            float o2[32];
-            sv::tmem_load_32(o_addr + D + d, o2);
+        for (int d = d0; d < d0 + width; d += 16) {
+          float o[16];
+          sv::tmem_load_16(from + d, o);
+          if (four) {
+            float o2[16];
+            sv::tmem_load_16(from + D + d, o2);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+            for (int e = 0; e < 16; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
           }
           if (!mine) continue;
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + d);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -1002,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (slot + prow) * D + d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         if (mine && d0 == 0) {
@@ -1055,8 +1092,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
       for (int e = 0; e < kE; ++e) o[e] = 0.f;
       for (int p = cut.first; p < main_grid; ++p) {
-        const long long from = share(cut.total, p, main_grid), to = share(cut.total, p + 1, main_grid);
-        if (from == to) continue;
+        const long long from = cut.shares.before(p);
+        if (from == cut.shares.before(p + 1)) break;
         if (p > cut.first && from - cut.start - kItemUnits >= cut.n) break;
         const long long at = (static_cast<long long>(p) * 2 + (p == cut.first ? 1 : 0)) * (kNT * kBlock) + r;
         const float2 ml = a.part_ml[at];
@@ -1187,16 +1224,11 @@ bool encode_tokens(CUtensorMap* map, int dtype, const void* base, int head_dim, 
                 {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(stride) * 2}, box_heads, box_tokens);
 }
 
-bool encode_entries(CUtensorMap* map, int dtype, const void* base, int64_t entry, int64_t rows) {
-  return encode(map, dtype, base, 2, {static_cast<uint64_t>(entry), static_cast<uint64_t>(rows), 1},
-                {static_cast<uint64_t>(entry) * 2, 0}, 1, 1);
-}
-
 template <typename T, int D, bool kPaged>
 spec_status launch(const AttnArgs& a, const CUtensorMap (&maps)[3], const sv::DeviceInfo& dev, cudaStream_t s) {
   using Sh = Shape<D, kPaged>;
   constexpr size_t kBytes = 1024 + Sh::kQBytes + Sh::kStages * Sh::kTileBytes + (sizeof(Sync) + 15) / 16 * 16 +
-                            (kPaged ? sizeof(PagedShared) : 0);
+                            sizeof(Exchange) + (kPaged ? sizeof(TreeShared) : 0);
   static_assert(kBytes <= 232448, "shared memory of one CTA");
   static_assert(kBytes > 116 * 1024, "one CTA per SM: it takes all of the tensor memory");
   static bool done[64] = {false};
@@ -1278,13 +1310,11 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   a.num_pages = dims.num_pages;
   a.max_pages = dims.max_pages;
   a.tile_tokens = kBlock / a.G;
-  const int64_t entry = 2ll * dims.kv_heads * dims.head_dim, tokens = static_cast<int64_t>(dims.B) * dims.S;
+  const int64_t tokens = static_cast<int64_t>(dims.B) * dims.S;
   CUtensorMap maps[3];
-  if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens) ||
-      !encode_entries(&maps[1], dims.dtype, pool, entry, static_cast<int64_t>(dims.num_pages) * dims.page_size) ||
-      !encode_entries(&maps[2], dims.dtype, staged ? staged : pool, entry,
-                      staged ? tokens : static_cast<int64_t>(dims.num_pages) * dims.page_size))
+  if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens))
     return SPEC_ERR_CUDA;
+  maps[1] = maps[2] = maps[0];  // (not used)
   return launch<true>(a, maps, dims.head_dim, dims.dtype, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
