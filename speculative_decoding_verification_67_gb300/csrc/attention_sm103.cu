@@ -56,9 +56,8 @@
 namespace {
 
 constexpr int kBlock = 128;          // keys per block, rows per tile
-constexpr int kSoftWarps = 16;       // two row tiles x two halves of the 128 score columns x 4 warps of 32 rows
-constexpr int kThreads = 640;        // softmax warps, an MMA warp, load warps
-constexpr int kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kThreads = 384;        // two softmax warpgroups, an MMA warp, two load warps, an idle one
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kCopyWarps = 2;        // load warps of the cache form
 constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
 constexpr int kItemUnits = 2;        // an item's start and end, in blocks
@@ -248,7 +247,7 @@ struct Sync {
   uint32_t tmem;
   int abort;
   int o_set[2];             // the softmax warps have written O themselves
-  unsigned spoiled[2][4][4];
+  unsigned spoiled[2][2][4];
   long long u0, u1, start;
   Shares shares;
   int b, kvh, tile;
@@ -257,9 +256,8 @@ struct Sync {
 };
 
 struct Exchange {
-  float top[2][2][kBlock];        // [tile][half][row] maxima of a block
   float ref[2][2][kBlock];        // [segment parity][tile][row]
-  float sum[2][2][2][kBlock];     // [segment parity][tile][half][row]
+  float sum[2][2][kBlock];
 };
 
 struct TreeShared {
@@ -281,26 +279,20 @@ __device__ __forceinline__ void await(Sync& sh, uint64_t* bar, uint32_t parity) 
   }
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ bool aborted(Sync& sh) { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; }
 
-// Named barriers of the softmax warps: 1 + t the 256 threads of a row tile,
+// Named barriers of the softmax warps: 1 + t the 128 threads of a row tile,
 // 3 those of both.
 __device__ __forceinline__ void meet(int id, int threads) {
   asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ bool meet_any(int id, int threads, bool mine) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %3, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned p, %1, %2, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(any)
-      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
-      : "memory");
-  return any != 0;
-}
-
 // 16 bytes global -> shared, zeros where `bytes` is 0 (the address is not read then).
 __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -406,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Sync& sh = *reinterpret_cast<Sync*>(tail);
   Exchange& ex = *reinterpret_cast<Exchange*>(tail + (sizeof(Sync) + 15) / 16 * 16);
   TreeShared& ts = *reinterpret_cast<TreeShared*>(&ex + 1);  // (cache only)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffle tells the compiler that the warp index is the same in all lanes)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x;
   const int grid = gridDim.x;
 
@@ -420,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     sv::mbar_init(&sh.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       sv::mbar_init(&sh.s_full[t], 1);
-      sv::mbar_init(&sh.p_full[t], 8);
+      sv::mbar_init(&sh.p_full[t], 4);
       sv::mbar_init(&sh.o_full[t], 1);
-      sv::mbar_init(&sh.o_free[t], kPaged ? 16 : 8);
+      sv::mbar_init(&sh.o_free[t], kPaged ? 8 : 4);
     }
     sv::mbar_init(&sh.done, 1);
     sv::fence_barrier_init();
@@ -641,7 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMA
-    if (lane == 0) {
+    // All lanes walk the loop, so that addresses stay in uniform registers; one issues.
+    {
+      const bool issuer = elect_one();
       uint32_t loads = 0, segs = 0, p_cnt[2] = {0, 0}, used[2] = {0, 0};
       constexpr uint32_t kIdS = idesc<T>(kBlock, kBlock, 0), kIdO = idesc<T>(kBlock, D, 1);
       const uint32_t ring_addr = sv::smem_u32(ring), q_addr = sv::smem_u32(q_tile);
@@ -652,15 +647,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         sv::tc_fence_after_sync();
         return ring_addr + slot * Sh::kTileBytes;
       };
+      auto commit = [&](uint64_t* bar) {
+        if (issuer) sv::mma_commit(bar);
+        __syncwarp();
+      };
       auto scores = [&](int t, uint32_t k_addr) {
-        const uint32_t qa = q_addr + (kPaged ? 0 : t * Sh::kTileBytes);
+        const uint32_t qa = __shfl_sync(0xffffffffu, q_addr + (kPaged ? 0 : t * Sh::kTileBytes), 0);
+        const uint32_t ka = __shfl_sync(0xffffffffu, k_addr, 0), d = __shfl_sync(0xffffffffu, tmem + t * kBlock, 0);
+        const uint64_t q_desc = sv::smem_desc_k_sw128(qa), k_desc = sv::smem_desc_k_sw128(ka);
+        if (issuer) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * (kBlock * 128) + (k % 4) * 32;
-          sv::mma_bf16_ss(tmem + t * kBlock, sv::smem_desc_k_sw128(qa + off), sv::smem_desc_k_sw128(k_addr + off), kIdS,
-                          k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k / 4) * (kBlock * 128) + (k % 4) * 32) >> 4;
+            sv::mma_bf16_ss(d, q_desc + off, k_desc + off, kIdS, k > 0);
+          }
+          sv::mma_commit(&sh.s_full[t]);
         }
-        sv::mma_commit(&sh.s_full[t]);
+        __syncwarp();
       };
       // P V of one block; waits for P and, first, for O to be free
       auto values = [&](int t, uint32_t v_addr, bool first) {
@@ -668,11 +671,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         await(sh, &sh.p_full[t], p_cnt[t] & 1);
         ++p_cnt[t];
         sv::tc_fence_after_sync();
-        const bool fresh = first && !*reinterpret_cast<volatile int*>(&sh.o_set[t]);
+        const uint32_t fresh = first && !*reinterpret_cast<volatile int*>(&sh.o_set[t]);
+        const uint32_t va = __shfl_sync(0xffffffffu, v_addr, 0), p = __shfl_sync(0xffffffffu, tmem + t * kBlock, 0);
+        const uint64_t v_desc = sv::smem_desc_mn_sw128(va, kBlock * 128);
+        const uint32_t go = __shfl_sync(0xffffffffu, fresh ^ 1u, 0), d = p - t * kBlock + Sh::kO + t * D;
+        if (issuer) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          sv::mma_f16_ts(tmem + Sh::kO + t * D, tmem + t * kBlock + (k & 3) * 8 + (k >> 2) * 64,
-                         sv::smem_desc_mn_sw128(v_addr + k * 2048, kBlock * 128), kIdO, !(fresh && k == 0));
+          for (int k = 0; k < kBlock / 16; ++k)
+            sv::mma_f16_ts(d, p + k * 8, v_desc + k * (2048 >> 4), kIdO, k > 0 ? 1u : go);
+        }
+        __syncwarp();
       };
       for (; at.start < u1; at.next(a)) {
         const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
@@ -684,20 +692,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2 && i < nb; ++i) {
             const uint32_t k_addr = arrived();
             scores(i, k_addr);
-            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
+            commit(&sh.empty[loads++ % Sh::kStages]);
           }
-          if (nb <= 2) sv::mma_commit(&sh.q_empty);
+          if (nb <= 2) commit(&sh.q_empty);
           for (int i = 0; i < nb; ++i) {
             const int t = i & 1;
             const uint32_t v_addr = arrived();
             values(t, v_addr, i < 2);
-            sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
-            if (i + 2 >= nb) sv::mma_commit(&sh.o_full[t]);
+            commit(&sh.empty[loads++ % Sh::kStages]);
+            if (i + 2 >= nb) commit(&sh.o_full[t]);
             if (i + 2 < nb) {
               const uint32_t k_addr = arrived();
                 scores(t, k_addr);
-              sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
-              if (i + 3 == nb) sv::mma_commit(&sh.q_empty);
+              commit(&sh.empty[loads++ % Sh::kStages]);
+              if (i + 3 == nb) commit(&sh.q_empty);
             }
           }
           ++used[0];
@@ -707,12 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t k_addr = arrived();
           scores(0, k_addr);
           if (two) scores(1, k_addr);
-          sv::mma_commit(&sh.empty[loads++ % Sh::kStages]);
-          if (nb == 1) sv::mma_commit(&sh.q_empty);
+          commit(&sh.empty[loads++ % Sh::kStages]);
+          if (nb == 1) commit(&sh.q_empty);
           for (int i = 0; i < nb; ++i) {
             const uint32_t v_addr = arrived(), v_slot = loads++ % Sh::kStages;
             values(0, v_addr, i == 0);
-            if (i + 1 == nb) sv::mma_commit(&sh.o_full[0]);
+            if (i + 1 == nb) commit(&sh.o_full[0]);
             uint32_t k_slot = 0;
             if (i + 1 < nb) {
               k_addr = arrived();
@@ -722,12 +730,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (two) {
               values(1, v_addr, i == 0);
               }
-            sv::mma_commit(&sh.empty[v_slot]);
-            if (two && i + 1 == nb) sv::mma_commit(&sh.o_full[1]);
+            commit(&sh.empty[v_slot]);
+            if (two && i + 1 == nb) commit(&sh.o_full[1]);
             if (i + 1 < nb) {
               if (two) scores(1, k_addr);
-              sv::mma_commit(&sh.empty[k_slot]);
-              if (i + 2 == nb) sv::mma_commit(&sh.q_empty);
+              commit(&sh.empty[k_slot]);
+              if (i + 2 == nb) commit(&sh.q_empty);
             }
           }
           ++used[0];
@@ -736,15 +744,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++segs;
       }
       if (aborted(sh)) {  // the products in flight end before the tensor memory is given back
-        sv::mma_commit(&sh.done);
+        commit(&sh.done);
         sv::mbar_wait(&sh.done, 0);
       }
     }
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
-    // thread: row `row` of tile t, score columns 64 half .. + 63
-    const int t = warp >> 3, half = (warp >> 2) & 1, row = tid & (kBlock - 1);
+    const int t = warp >> 2, row = tid & (kBlock - 1);             // one row of one tile per thread
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_addr = tmem + t * kBlock + lanes;
     const uint32_t o_addr = tmem + Sh::kO + t * D + lanes;
@@ -787,8 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int committed = kPaged && a.staged ? blocks_of(s.base) : at.n;
       const bool tree = kPaged && a.parents != nullptr;
       if (tree) {
-        meet(1 + t, 256);  // the last segment's readers are done
-        if (half == 0 && alive) {
+        if (alive) {
           unsigned* anc = ts.anc[t][row];
 #pragma unroll
           for (int w = 0; w < 8; ++w) anc[w] = 0;
@@ -799,9 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p = up < p ? up : -1;  // (a bad parent is flagged; the walk still ends)
           }
         }
-        meet(1 + t, 256);
       }
-      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of this half's weights
+      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of its weights
       float top = -INFINITY;             // the same reference as a score
 
       for (int i = kPaged ? t : 0; i < nb; i += kPaged ? 2 : 1) {
@@ -826,10 +831,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         sv::tc_fence_after_sync();
         unsigned spoil[4] = {0, 0, 0, 0};
         if (look) {
-          // the V tile's rows (one per thread of a half), each thread a share of the columns
+          // one row of the V tile per thread; where both tiles read it, each half of the row
           const bool pair = !kPaged && both;
-          const int parts = pair ? 4 : 2, part = pair ? 2 * t + half : half, box = pair ? 0 : t;
-          const int bar = pair ? 3 : 1 + t, crowd = pair ? 512 : 256;
+          const int parts = pair ? 2 : 1, part = pair ? t : 0, box = pair ? 0 : t;
+          const int bar = pair ? 3 : 1 + t, crowd = pair ? 256 : 128;
           const uint32_t rank = loads + v_rank<kPaged>(i, nb), slot = rank % Sh::kStages;
           wait(&sh.full[slot], rank / Sh::kStages & 1);
           uint8_t* vrow = ring + slot * Sh::kTileBytes + row * 128;
@@ -863,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const bool spoils = (spoil[0] | spoil[1] | spoil[2] | spoil[3]) != 0;
-        if (first && half == 0 && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
+        if (first && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
         // bit c of word w: column 32 w + c is seen
         auto seen_word = [&](int w) -> unsigned {
           if (tree && (fresh || !a.staged)) {
@@ -877,62 +882,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           return seen >= 32 * (w + 1) ? 0xffffffffu : (seen <= 32 * w ? 0u : (1u << (seen - 32 * w)) - 1u);
         };
         auto read = [&](int h, float (&x)[32]) {  // 32 scores, -infinity where the row must not see the key
-          sv::tmem_load_32(s_addr + 64 * half + 32 * h, x);
+          sv::tmem_load_32(s_addr + 32 * h, x);
           if (!masked) return;
-          const unsigned m = seen_word(2 * half + h);
+          const unsigned m = seen_word(h);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!(m >> c & 1u)) x[c] = -INFINITY;
         };
-        bool raise = false;
-        float blk = -INFINITY;
         if (alive) {
+          // One pass over the scores gives their maximum and, against the reference so far, their weights.  The
+          // weights stand if no row of the warp raises its reference; otherwise (always in the first block) they
+          // are taken again.  Nothing is written over the scores until then.
+          float2 acc[2];
+          uint32_t w[64];
+          for (bool settled = false;; settled = true) {
+            const float off = ref == -INFINITY ? 0.f : -ref;
+            const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            acc[0] = acc[1] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x[32];
-            read(h, x);
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+            for (int h = 0; h < 4; ++h) {
+              float x[32];
+              read(h, x);
+              if (!settled) {
 #pragma unroll
-            for (int c = 4; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-            blk = fmaxf(blk, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          }
-          // raise the reference where a weight would exceed 2^kSlack
-          raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
-        }
-        if (meet_any(1 + t, 256, raise || spoils)) {
-          ex.top[t][half][row] = blk;
-          meet(1 + t, 256);
-          if (alive) {
-            blk = fmaxf(blk, ex.top[t][half ^ 1][row]);
-            raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+                for (int c = 0; c < 32; c += 2) mx[c / 2 & 3] = fmaxf(mx[c / 2 & 3], fmaxf(x[c], x[c + 1]));
+              }
+              if (settled || !first) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  float2 z = fma2(make_float2(x[2 * e], x[2 * e + 1]), cc, oo);
+                  z.x = exp2_approx(z.x);
+                  z.y = exp2_approx(z.y);
+                  acc[e & 1] = add2(acc[e & 1], z);
+                  w[16 * h + e] = pack2(z.x, z.y, T());
+                }
+              }
+            }
+            if (settled) break;
+            const float blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // raise the reference where a weight would exceed 2^kSlack
+            const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+            const bool lift = __any_sync(0xffffffffu, raise);
+            if (!lift && !spoils && !first) break;
             const float was = ref;
             if (raise) {
               top = blk;
               ref = top * c2;
             }
-            if (!first && __any_sync(0xffffffffu, raise)) {
+            if (lift && !first) {
               const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
               sum *= f;
 #pragma unroll 1
-              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+              for (int c = 0; c < D; c += 32) {
                 float o[32];
                 sv::tmem_load_32(o_addr + c, o);
-                uint32_t w[32];
+                uint32_t u[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-                sv::tmem_store_32(o_addr + c, w);
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                sv::tmem_store_32(o_addr + c, u);
               }
               sv::tmem_wait_st();
             }
             if (spoils) {  // rare: values that are infinite or not a number, for the rows that see them
-              const float off = ref == -INFINITY ? 0.f : -ref;
+              const float off2 = ref == -INFINITY ? 0.f : -ref;
               if (first) {
                 if (used[t] > 0) wait(&sh.o_free[t], (used[t] - 1) & 1);
                 sv::tc_fence_after_sync();
-                uint32_t w[32];
+                uint32_t u[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = 0;
-                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) sv::tmem_store_32(o_addr + c, w);
+                for (int e = 0; e < 32; ++e) u[e] = 0;
+                for (int c = 0; c < D; c += 32) sv::tmem_store_32(o_addr + c, u);
                 sv::tmem_wait_st();
               }
 #pragma unroll 1
@@ -940,43 +960,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
                 if (!(sw >> (c & 31) & 1u)) continue;
                 const bool mine = seen_word(c >> 5) >> (c & 31) & 1u;
-                const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c), c2, off));
+                const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c), c2, off2));
                 const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
 #pragma unroll 1
-                for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 32) {
+                for (int d = 0; d < D; d += 32) {
                   float o[32];
                   sv::tmem_load_32(o_addr + d, o);
-                  uint32_t w[32];
+                  uint32_t u[32];
 #pragma unroll
                   for (int e = 0; e < 32; ++e)
-                    w[e] = __float_as_uint(mine && v != nullptr ? o[e] + p * to_f(v[d + e]) : o[e]);
-                  sv::tmem_store_32(o_addr + d, w);
+                    u[e] = __float_as_uint(mine && v != nullptr ? o[e] + p * to_f(v[d + e]) : o[e]);
+                  sv::tmem_store_32(o_addr + d, u);
                   sv::tmem_wait_st();
                 }
               }
             }
           }
-          if (spoils) meet(1 + t, 256);  // either half has read the other's scores
-        }
-        if (alive) {
-          const float off = ref == -INFINITY ? 0.f : -ref;
-          const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x[32];
-            read(h, x);  // again, rather than held meanwhile; the weights are written over scores read before
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 z = fma2(make_float2(x[2 * e], x[2 * e + 1]), cc, oo);
-              z.x = exp2_approx(z.x);
-              z.y = exp2_approx(z.y);
-              acc[e & 1] = add2(acc[e & 1], z);
-              w[e] = pack2(z.x, z.y, T());
-            }
-            sv::tmem_store_16(s_addr + half * 64 + h * 16, w);
-          }
+          sv::tmem_store_32(s_addr, w);
+          sv::tmem_store_32(s_addr + 32, w + 32);
           const float2 both_acc = add2(acc[0], acc[1]);
           sum += both_acc.x + both_acc.y;
           sv::tmem_wait_st();
@@ -991,22 +992,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = lo == 0 && hi == at.n;
       const long long slot = (static_cast<long long>(cta) * 2 + (lo > 0 ? 0 : 1)) * (kNT * kBlock);
       const uint32_t par = merges++ & 1;
-      if (half == 0) ex.ref[par][t][row] = ref;
-      ex.sum[par][t][half][row] = sum;
-      // the warps that share the rows' columns: two, or in the cache form with both tiles in use four
-      const bool four = kPaged && both;
-      meet(four ? 3 : 1 + t, four ? 512 : 256);
-      const int t0 = kPaged ? 0 : t, width = four ? D / 4 : D / 2, d0 = (four ? 2 * t + half : half) * width;
-      float f0 = 1.f, f1 = 0.f, all = ex.sum[par][t0][0][row] + ex.sum[par][t0][1][row], base2 = ex.ref[par][t0][row];
-      if (four) {
-        const float m0 = base2, m1 = ex.ref[par][1][row];
+      // in the cache form with both tiles in use each has half of the rows' columns
+      const bool joint = kPaged && both;
+      const int t0 = kPaged ? 0 : t, width = joint ? D / 2 : D, d0 = joint ? t * width : 0;
+      float f0 = 1.f, f1 = 0.f, all = sum, base2 = ref;
+      if (joint) {
+        ex.ref[par][t][row] = ref;
+        ex.sum[par][t][row] = sum;
+        meet(3, 256);
+        const float m0 = ex.ref[par][0][row], m1 = ex.ref[par][1][row];
         base2 = fmaxf(m0, m1);
         f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - base2);
         f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - base2);
-        all = all * f0 + (ex.sum[par][1][0][row] + ex.sum[par][1][1][row]) * f1;
+        all = ex.sum[par][0][row] * f0 + ex.sum[par][1][row] * f1;
       }
       wait(&sh.o_full[t0], used[t0] & 1);
-      if (four) wait(&sh.o_full[1], used[1] & 1);
+      if (joint) wait(&sh.o_full[1], used[1] & 1);
       sv::tc_fence_after_sync();
       if (alive) {
         const bool mine = row < rows;
@@ -1019,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = d0; d < d0 + width; d += 16) {
           float o[16];
           sv::tmem_load_16(from + d, o);
-          if (four) {
+          if (joint) {
             float o2[16];
             sv::tmem_load_16(from + D + d, o2);
 #pragma unroll
