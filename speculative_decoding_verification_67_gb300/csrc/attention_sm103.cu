@@ -881,56 +881,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return seen >= 32 * (w + 1) ? 0xffffffffu : (seen <= 32 * w ? 0u : (1u << (seen - 32 * w)) - 1u);
         };
-        auto read = [&](int h, float (&x)[32]) {  // 32 scores, -infinity where the row must not see the key
-          sv::tmem_load_32(s_addr + 32 * h, x);
+        // 32 scores as they arrive, -infinity where the row must not see the key
+        auto hide = [&](int h, uint32_t (&x)[32]) {
+          sv::tmem_arrived_32(x);
           if (!masked) return;
           const unsigned m = seen_word(h);
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (!(m >> c & 1u)) x[c] = -INFINITY;
+            if (!(m >> c & 1u)) x[c] = 0xff800000u;
         };
         if (alive) {
-          // One pass over the scores gives their maximum and, against the reference so far, their weights.  The
-          // weights stand if no row of the warp raises its reference; otherwise (always in the first block) they
-          // are taken again.  Nothing is written over the scores until then.
-          float2 acc[2];
-          uint32_t w[64];
-          for (bool settled = false;; settled = true) {
-            const float off = ref == -INFINITY ? 0.f : -ref;
-            const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            acc[0] = acc[1] = make_float2(0.f, 0.f);
+          // Two passes over the scores, each with the next 32 columns on their way while the last ones are worked on:
+          // their maximum, then their weights, written over scores read before.
+          uint32_t x[2][32];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          sv::tmem_start_32(s_addr, x[0]);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              float x[32];
-              read(h, x);
-              if (!settled) {
+          for (int h = 0; h < 4; ++h) {
+            uint32_t(&now)[32] = x[h & 1];
+            hide(h, now);
+            sv::tmem_start_32(s_addr + 32 * ((h + 1) & 3), x[(h + 1) & 1]);
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) mx[c / 2 & 3] = fmaxf(mx[c / 2 & 3], fmaxf(x[c], x[c + 1]));
-              }
-              if (settled || !first) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  float2 z = fma2(make_float2(x[2 * e], x[2 * e + 1]), cc, oo);
-                  z.x = exp2_approx(z.x);
-                  z.y = exp2_approx(z.y);
-                  acc[e & 1] = add2(acc[e & 1], z);
-                  w[16 * h + e] = pack2(z.x, z.y, T());
-                }
-              }
-            }
-            if (settled) break;
-            const float blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // raise the reference where a weight would exceed 2^kSlack
-            const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
-            const bool lift = __any_sync(0xffffffffu, raise);
-            if (!lift && !spoils && !first) break;
+            for (int c = 0; c < 32; c += 2)
+              mx[c / 2 & 3] = fmaxf(mx[c / 2 & 3], fmaxf(__uint_as_float(now[c]), __uint_as_float(now[c + 1])));
+          }
+          const float blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // raise the reference where a weight would exceed 2^kSlack
+          const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
+          if (__any_sync(0xffffffffu, raise) || spoils) {
+            sv::tmem_arrived_32(x[0]);  // its registers are free from here on
             const float was = ref;
             if (raise) {
               top = blk;
               ref = top * c2;
             }
-            if (lift && !first) {
+            if (!first) {
               const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
               sum *= f;
 #pragma unroll 1
@@ -975,9 +960,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
+
+            sv::tmem_start_32(s_addr, x[0]);
           }
-          sv::tmem_store_32(s_addr, w);
-          sv::tmem_store_32(s_addr + 32, w + 32);
+          const float off = ref == -INFINITY ? 0.f : -ref;
+          const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t(&now)[32] = x[h & 1];
+            hide(h, now);
+            if (h < 3) sv::tmem_start_32(s_addr + 32 * (h + 1), x[(h + 1) & 1]);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 z = fma2(make_float2(__uint_as_float(now[2 * e]), __uint_as_float(now[2 * e + 1])), cc, oo);
+              z.x = exp2_approx(z.x);
+              z.y = exp2_approx(z.y);
+              acc[e & 1] = add2(acc[e & 1], z);
+              w[e] = pack2(z.x, z.y, T());
+            }
+            sv::tmem_store_16(s_addr + 16 * h, w);
+          }
           const float2 both_acc = add2(acc[0], acc[1]);
           sum += both_acc.x + both_acc.y;
           sv::tmem_wait_st();
