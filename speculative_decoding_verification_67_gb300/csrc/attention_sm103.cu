@@ -56,9 +56,9 @@
 namespace {
 
 constexpr int kBlock = 128;          // keys per block, rows per tile
-constexpr int kThreads = 384;        // two softmax warpgroups, an MMA warp, two load warps, an idle one
+constexpr int kThreads = 384;        // two softmax warpgroups, an MMA warp, three load warps
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kCopyWarps = 2;        // load warps of the cache form
+constexpr int kCopyWarps = 3;        // load warps of the cache form
 constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
 constexpr int kItemUnits = 2;        // an item's start and end, in blocks
 constexpr int kMaxTree = 256;
@@ -110,6 +110,7 @@ struct AttnArgs {
   float scale_log2;
   int B, S, heads, kv_heads, G, page_size, num_pages, max_pages, total_q, total_k;
   int tile_tokens;        // whole tokens in a row tile
+  int box;                // rows of one page box (a divisor of the page and of a block), or 0: row by row
   long long k_stride, v_stride;
   // workspace
   int* ctrl;
@@ -387,7 +388,7 @@ template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
-  // (map_k and map_v: prompts only)
+  // (cache: map_k is the pool's; map_v is not used)
   using Sh = Shape<D, kPaged>;
   constexpr int kNT = kTiles<kPaged>;
   extern __shared__ uint8_t raw[];
@@ -428,10 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kLoadWarp && lane == 0) {
     sv::prefetch_tensor_map(&map_q);
-    if (!kPaged) {
-      sv::prefetch_tensor_map(&map_k);
-      sv::prefetch_tensor_map(&map_v);
-    }
+    sv::prefetch_tensor_map(&map_k);
+    if (!kPaged) sv::prefetch_tensor_map(&map_v);
   }
 
   // ---- this CTA's share of the units: a scan over the sequences
@@ -529,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t loads = 0, segs = 0;
     const uint64_t keep = sv::l2_policy_evict_last(), once = sv::l2_policy_evict_first();
     const int lw = warp - kLoadWarp;
+    const bool issuer = elect_one();
+    const uint64_t policy = a.S * a.G <= kBlock ? once : keep;  // whether another row tile reads the entries again
     auto load_q = [&]() {  // by one thread
       if (segs > 0) await(sh, &sh.q_empty, (segs - 1) & 1);
       if (aborted(sh)) return;
@@ -549,25 +550,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int limit = a.staged ? at.s.base : at.s.base + at.s.Lq;
           const int* table = a.bt + static_cast<long long>(at.b) * a.max_pages;
           const long long entry = 4ll * a.kv_heads * D;  // bytes
-          constexpr int kRows = kBlock / kCopyWarps;     // rows of a tile this warp copies
-          constexpr int kEach = kRows / 32;              // rows a lane looks up: lane, lane + 32, ..
+          constexpr int kEach = kBlock / 32;             // rows a lane looks up: lane, lane + 32, ..
           constexpr int kChunks = D / 8;                 // 16-byte pieces of a row
           constexpr int kAtOnce = 32 / kChunks;          // rows one instruction copies
           const int chunk = lane % kChunks, sub = lane / kChunks;
           int r0[kEach], r1[kEach] = {};  // rows of the block before, of this block; -1: zeros
+          // whole blocks of the pool come in boxes of a.box rows of one page, the others row by row
+          auto boxed = [&](int j) { return a.box != 0 && j < committed && (j + 1) * kBlock <= limit; };
+          auto row_at = [&](int p) {  // the pool's row of a position
+            const int col = p / a.page_size, page = table[col];
+            if (page >= 0 && page < a.num_pages) return page * a.page_size + (p - col * a.page_size);
+            atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
+            return -1;
+          };
           auto rows_of = [&](int j, int (&r)[kEach]) {
+            if (boxed(j)) {  // lane i: first row of box i
+              r[0] = lane * a.box < kBlock ? row_at(j * kBlock + lane * a.box) : 0;
+              if (r[0] < 0) r[0] = a.num_pages * a.page_size;  // (outside the tensor: zeros)
+              return;
+            }
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-              const int in = lw * kRows + 32 * e + lane;
+              const int in = 32 * e + lane;
               r[e] = -1;
               if (j >= committed) {
                 const int i = (j - committed) * kBlock + in;
                 if (i < at.s.Lq) r[e] = at.b * a.S + i;
               } else if (j * kBlock + in < limit) {
-                const int p = j * kBlock + in, col = p / a.page_size;
-                const int page = table[col];
-                if (page >= 0 && page < a.num_pages) r[e] = page * a.page_size + (p - col * a.page_size);
-                else atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
+                r[e] = row_at(j * kBlock + in);
               }
             }
           };
@@ -575,17 +585,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t slot = loads % Sh::kStages;
             await(sh, &sh.empty[slot], (loads / Sh::kStages & 1) ^ 1);
             ++loads;
-            if (aborted(sh)) return;
+            if (__any_sync(0xffffffffu, aborted(sh))) return;
+            if (boxed(j)) {
+              const int boxes = kBlock / a.box;
+              uint8_t* dst = ring + slot * Sh::kTileBytes;
+              const int mine = boxes > lw ? (boxes - lw + kCopyWarps - 1) / kCopyWarps : 0;  // boxes lw, lw + 3, ..
+              if (issuer) {
+                if (mine > 0) sv::mbar_arrive_expect_tx(&sh.full[slot], mine * a.box * D * 2);
+                else sv::mbar_arrive(&sh.full[slot]);
+              } else {
+                sv::mbar_arrive(&sh.full[slot]);
+              }
+              __syncwarp();
+              for (int i = lw; i < boxes; i += kCopyWarps) {
+                const int row = __shfl_sync(0xffffffffu, r[0], i);
+                if (issuer) {
+#pragma unroll
+                  for (int h = 0; h < D / 64; ++h)
+                    sv::tma_load_2d(dst + h * (kBlock * 128) + i * a.box * 128, &map_k, &sh.full[slot],
+                                    head * D + h * 64, row, policy);
+                }
+                __syncwarp();
+              }
+              return;
+            }
             const char* from = static_cast<const char*>(j >= committed ? a.staged : a.k) + head * (D * 2) + chunk * 16;
             const uint32_t to = sv::smem_u32(ring + slot * Sh::kTileBytes) + (chunk >> 3) * (kBlock * 128);
 #pragma unroll
-            for (int i = 0; i < kRows / kAtOnce; ++i) {
-              const int in = i * kAtOnce + sub;                   // row within this warp's
-              const int e = i * kAtOnce / 32;                     // (the same for the whole warp)
-              const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
-              const int spot = lw * kRows + in;
-              copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + (row < 0 ? 0 : row * entry),
-                      row < 0 ? 0 : 16);
+            for (int e = 0; e < kEach; ++e) {
+#pragma unroll 2
+              for (int i = (lw + e) % kCopyWarps; i < 32 / kAtOnce; i += kCopyWarps) {
+                const int in = i * kAtOnce + sub, spot = 32 * e + in;
+                const int row = __shfl_sync(0xffffffffu, r[e], in);
+                copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + (row < 0 ? 0 : row * entry),
+                        row < 0 ? 0 : 16);
+              }
             }
             copies_arrive(&sh.full[slot]);
           };
@@ -624,10 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
       }
       if (aborted(sh) && lane == 0) {  // leave no copy in flight
-        if (!kPaged) {
-          const uint32_t first = loads > Sh::kStages ? loads - Sh::kStages : 0;
-          for (uint32_t i = first; i < loads; ++i) sv::mbar_wait(&sh.full[i % Sh::kStages], i / Sh::kStages & 1);
-        }
+        const uint32_t last = loads > Sh::kStages ? loads - Sh::kStages : 0;
+        for (uint32_t i = last; i < loads; ++i) sv::mbar_wait(&sh.full[i % Sh::kStages], i / Sh::kStages & 1);
         if (lw == 0 && segs > 0) sv::mbar_wait(&sh.q_full, (segs - 1) & 1);
       }
       __syncwarp();
@@ -1319,7 +1351,16 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   CUtensorMap maps[3];
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens))
     return SPEC_ERR_CUDA;
-  maps[1] = maps[2] = maps[0];  // (not used)
+  // Boxes of at least eight rows; below that one copy of 16 bytes per thread is faster.
+  a.box = kBlock;
+  while (a.box >= 8 && dims.page_size % a.box != 0) a.box /= 2;
+  if (a.box < 8) a.box = 0;
+  const int64_t entry = 2ll * dims.kv_heads * dims.head_dim;
+  if (!encode(&maps[1], dims.dtype, pool, 2,
+              {static_cast<uint64_t>(entry), static_cast<uint64_t>(dims.num_pages) * dims.page_size, 1},
+              {static_cast<uint64_t>(entry) * 2, 0}, a.box ? a.box : 1, 1))
+    return SPEC_ERR_CUDA;
+  maps[2] = maps[1];  // (not used)
   return launch<true>(a, maps, dims.head_dim, dims.dtype, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
