@@ -29,6 +29,7 @@ Names follow the C ABI:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -633,23 +634,23 @@ def _one_device(first, name, *others):
 class _Launch:
     """Makes ``stream`` (default: the current stream of ``device``) and its
     device current for the call, so that what is allocated in it belongs to
-    the stream the kernels run on."""
-    __slots__ = ("stream", "context")
+    the stream the kernels run on.  Entering gives the raw stream handle."""
+    __slots__ = ("raw", "context")
 
     def __init__(self, device, stream):
         if stream is None:
-            self.stream = torch.cuda.current_stream(device)
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
             self.context = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
         else:
             if stream.device != device:
                 raise ValueError(f"the stream belongs to {stream.device}, the tensors lie on {device}")
-            self.stream = stream
+            self.raw = stream.cuda_stream
             self.context = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.context is not None:
             self.context.__enter__()
-        return self.stream.cuda_stream
+        return self.raw
 
     def __exit__(self, *exc):
         if self.context is not None:
@@ -657,7 +658,7 @@ class _Launch:
 
 
 def _int32(t, name, shape):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
@@ -699,37 +700,40 @@ def _attn_dtype(q, *others):
     return code
 
 
-def _token_stride(t, name):
+def _token_stride(shape, strides, name):
     """Elements from one token to the next of [tokens][heads][head_dim], heads dense."""
-    heads, D = t.shape[-2:]
-    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+    heads, D = shape[-2:]
+    if strides[-1] != 1 or (heads > 1 and strides[-2] != D):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    if t.shape[-3] == 1:
-        return heads * D if t.dim() == 3 or t.shape[0] == 1 else t.stride(0)
-    stride = t.stride(-3)
-    if t.dim() == 4 and t.shape[0] > 1 and t.stride(0) != t.shape[1] * stride:
+    if shape[-3] == 1:
+        return heads * D if len(shape) == 3 or shape[0] == 1 else strides[0]
+    stride = strides[-3]
+    if len(shape) == 4 and shape[0] > 1 and strides[0] != shape[1] * stride:
         raise ValueError(f"the tokens of {name} must be evenly spaced")
     return stride
 
 
-def _kv_attn_dims(q, pool, max_pages):
-    if q.dim() != 4:
+# The sizes of a call and the bytes of its workspace, by shapes and types alone.
+@functools.lru_cache(maxsize=1024)
+def _kv_attn_plan(q_shape, q_strides, dtype, pool_shape, max_pages):
+    if len(q_shape) != 4:
         raise ValueError("q must be [B][S][heads][head_dim]")
-    if pool.dim() != 3 or not pool.is_contiguous():
+    if len(pool_shape) != 3:
         raise ValueError("pool must be one layer's contiguous plane [num_pages][page_size][entry]")
-    B, S, heads, D = q.shape
-    kv_heads, rest = divmod(pool.shape[2], 2 * D)
+    B, S, heads, D = q_shape
+    kv_heads, rest = divmod(pool_shape[2], 2 * D) if D else (0, 1)
     if rest:
-        raise ValueError(f"an entry of {pool.shape[2]} elements is not [2][kv_heads][{D}]")
-    return SpecKvAttnDims(B, S, heads, kv_heads, D, pool.shape[1], pool.shape[0], max_pages, _attn_dtype(q, pool),
-                          _token_stride(q, "q"))
+        raise ValueError(f"an entry of {pool_shape[2]} elements is not [2][kv_heads][{D}]")
+    dims = SpecKvAttnDims(B, S, heads, kv_heads, D, pool_shape[1], pool_shape[0], max_pages, dtype,
+                          _token_stride(q_shape, q_strides, "q"))
+    return dims, int(library().spec_kv_attention_workspace_bytes(dims)), 1.0 / math.sqrt(D)
 
 
 def kv_attention_workspace(q, pool) -> torch.Tensor:
     """A zeroed workspace for :func:`spec_kv_attention` calls shaped like ``q``
     and ``pool`` (reusable; each call leaves it ready for the next)."""
-    dims = _kv_attn_dims(q, pool, 1)
-    return _scratch(None, library().spec_kv_attention_workspace_bytes(dims), _one_device(q, "q", pool))
+    plan = _kv_attn_plan(q.shape, q.stride(), _attn_dtype(q, pool), pool.shape, 1)
+    return _scratch(None, plan[1], _one_device(q, "q", pool))
 
 
 def spec_kv_attention(q, pool, block_table, seq_len, staged=None, *, parents=None, q_len=None, scale=None, out=None,
@@ -747,10 +751,13 @@ def spec_kv_attention(q, pool, block_table, seq_len, staged=None, *, parents=Non
     receives the log-sum-exp where given."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B][max_pages]")
-    dims = _kv_attn_dims(q, pool, block_table.shape[1])
-    B, S = q.shape[:2]
+    shape = q.shape
+    dims, nbytes, usual = _kv_attn_plan(shape, q.stride(), _attn_dtype(q, pool, staged, out), pool.shape,
+                                        block_table.shape[1])
+    B, S = shape[:2]
     dev = _one_device(q, "q", pool, block_table, seq_len, staged, parents, q_len, out, out_lse, workspace)
-    _attn_dtype(q, staged, out)
+    if not pool.is_contiguous():
+        raise ValueError("pool must be one layer's contiguous plane [num_pages][page_size][entry]")
     _int32(block_table, "block_table", (B, dims.max_pages))
     _int32(seq_len, "seq_len", (B,))
     if staged is not None and (staged.shape != (B, S, pool.shape[2]) or not staged.is_contiguous()):
@@ -759,36 +766,38 @@ def spec_kv_attention(q, pool, block_table, seq_len, staged=None, *, parents=Non
         _int32(parents, "parents", (B, S))
     if q_len is not None:
         _int32(q_len, "q_len", (B,))
-    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
-        raise ValueError(f"out must be contiguous {tuple(q.shape)}")
-    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != q.shape[:3]
+    if out is not None and (out.shape != shape or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous {tuple(shape)}")
+    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != shape[:3]
                                 or not out_lse.is_contiguous()):
-        raise ValueError(f"out_lse must be contiguous float32 {tuple(q.shape[:3])}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(dims.head_dim)
-    lib = library()
+        raise ValueError(f"out_lse must be contiguous float32 {tuple(shape[:3])}")
     with _Launch(dev, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        workspace = _scratch(workspace, lib.spec_kv_attention_workspace_bytes(dims), dev)
-        _check(lib.spec_kv_attention(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seq_len.data_ptr(),
-                                     _at(staged), _at(parents), _at(q_len), scale, out.data_ptr(), _at(out_lse), dims,
-                                     workspace.data_ptr(), workspace.numel(), s))
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        workspace = _scratch(workspace, nbytes, dev)
+        _check(library().spec_kv_attention(
+            q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seq_len.data_ptr(), _at(staged), _at(parents),
+            _at(q_len), usual if scale is None else scale, out.data_ptr(), _at(out_lse), dims, workspace.data_ptr(),
+            workspace.numel(), s))
     return out
 
 
-def _prompt_dims(q, k, v, B):
-    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or k.shape[2] != q.shape[2]:
+@functools.lru_cache(maxsize=1024)
+def _prompt_plan(q_shape, q_strides, k_shape, k_strides, v_shape, v_strides, dtype, B):
+    if len(q_shape) != 3 or len(k_shape) != 3 or v_shape != k_shape or k_shape[2] != q_shape[2]:
         raise ValueError("q must be [total_q][heads][head_dim], k and v [total_k][kv_heads][head_dim]")
-    return SpecPromptDims(B, q.shape[1], k.shape[1], q.shape[2], q.shape[0], k.shape[0], _attn_dtype(q, k, v),
-                          _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"))
+    dims = SpecPromptDims(B, q_shape[1], k_shape[1], q_shape[2], q_shape[0], k_shape[0], dtype,
+                          _token_stride(q_shape, q_strides, "q"), _token_stride(k_shape, k_strides, "k"),
+                          _token_stride(v_shape, v_strides, "v"))
+    return dims, int(library().spec_prompt_attention_workspace_bytes(dims)), \
+        1.0 / math.sqrt(q_shape[2]) if q_shape[2] else 0.0
 
 
 def prompt_attention_workspace(q, k, B: int) -> torch.Tensor:
     """A zeroed workspace for :func:`spec_prompt_attention` calls on ``B``
     sequences shaped like ``q`` and ``k`` (reusable)."""
-    dims = _prompt_dims(q, k, k, B)
-    return _scratch(None, library().spec_prompt_attention_workspace_bytes(dims), _one_device(q, "q", k))
+    plan = _prompt_plan(q.shape, q.stride(), k.shape, k.stride(), k.shape, k.stride(), _attn_dtype(q, k), B)
+    return _scratch(None, plan[1], _one_device(q, "q", k))
 
 
 def spec_prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out_lse=None, workspace=None,
@@ -802,27 +811,25 @@ def spec_prompt_attention(q, k, v, cu_q, cu_k=None, *, scale=None, out=None, out
     if cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError("cu_q must be [B + 1]")
     B = cu_q.shape[0] - 1
-    dims = _prompt_dims(q, k, v, B)
+    shape = q.shape
+    dims, nbytes, usual = _prompt_plan(shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+                                       _attn_dtype(q, k, v, out), B)
     dev = _one_device(q, "q", k, v, cu_q, cu_k, out, out_lse, workspace)
-    _attn_dtype(q, out)
     _int32(cu_q, "cu_q", (B + 1,))
     if cu_k is not None:
         _int32(cu_k, "cu_k", (B + 1,))
-    if out is not None and (out.shape != q.shape or not out.is_contiguous()):
-        raise ValueError(f"out must be contiguous {tuple(q.shape)}")
-    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != q.shape[:2]
+    if out is not None and (out.shape != shape or not out.is_contiguous()):
+        raise ValueError(f"out must be contiguous {tuple(shape)}")
+    if out_lse is not None and (out_lse.dtype != torch.float32 or out_lse.shape != shape[:2]
                                 or not out_lse.is_contiguous()):
-        raise ValueError(f"out_lse must be contiguous float32 {tuple(q.shape[:2])}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(dims.head_dim)
-    lib = library()
+        raise ValueError(f"out_lse must be contiguous float32 {tuple(shape[:2])}")
     with _Launch(dev, stream) as s:
         if out is None:
-            out = torch.zeros(q.shape, dtype=q.dtype, device=dev)
-        workspace = _scratch(workspace, lib.spec_prompt_attention_workspace_bytes(dims), dev)
-        _check(lib.spec_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _at(cu_k), scale,
-                                         out.data_ptr(), _at(out_lse), dims, workspace.data_ptr(), workspace.numel(),
-                                         s))
+            out = torch.zeros(shape, dtype=q.dtype, device=dev)
+        workspace = _scratch(workspace, nbytes, dev)
+        _check(library().spec_prompt_attention(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), _at(cu_k), usual if scale is None else scale,
+            out.data_ptr(), _at(out_lse), dims, workspace.data_ptr(), workspace.numel(), s))
     return out
 
 
@@ -836,16 +843,23 @@ def attention_read_error(workspace, stream=None) -> int:
 KV_DEVERR_PATH, KV_DEVERR_REF, KV_DEVERR_PAIR, KV_DEVERR_BUSY, KV_DEVERR_POOL = 8, 16, 32, 64, 128
 
 
-def _pages(block_table, ref_count, page_size, seq_len, *others):
-    if block_table.dim() != 2 or ref_count.dim() != 1:
+@functools.lru_cache(maxsize=1024)
+def _pages_plan(table_shape, pages_shape, page_size):
+    if len(table_shape) != 2 or len(pages_shape) != 1:
         raise ValueError("block_table must be [B][max_pages] and ref_count [num_pages]")
+    dims = SpecKvPagesDims(table_shape[0], table_shape[1], pages_shape[0], page_size)
+    return dims, int(library().spec_kv_pages_workspace_bytes(dims))
+
+
+def _pages(block_table, ref_count, page_size, seq_len, *others):
+    shape = block_table.shape
+    dims, nbytes = _pages_plan(shape, ref_count.shape, page_size)
     dev = _one_device(block_table, "block_table", ref_count, seq_len, *others)
-    dims = SpecKvPagesDims(block_table.shape[0], block_table.shape[1], ref_count.shape[0], page_size)
-    _int32(block_table, "block_table", (dims.B, dims.max_pages))
-    _int32(ref_count, "ref_count", (dims.num_pages,))
+    _int32(block_table, "block_table", shape)
+    _int32(ref_count, "ref_count", ref_count.shape)
     if seq_len is not None:
-        _int32(seq_len, "seq_len", (dims.B,))
-    return dev, dims
+        _int32(seq_len, "seq_len", shape[:1])
+    return dev, dims, nbytes
 
 
 def _pool_planes(pool, num_pages):
@@ -856,8 +870,8 @@ def _pool_planes(pool, num_pages):
 
 def kv_pages_workspace(block_table, ref_count) -> torch.Tensor:
     """A zeroed workspace for the page operators on this table and pool (reusable)."""
-    dev, dims = _pages(block_table, ref_count, 1, None)
-    return _scratch(None, library().spec_kv_pages_workspace_bytes(dims), dev)
+    dev, _, nbytes = _pages(block_table, ref_count, 1, None)
+    return _scratch(None, nbytes, dev)
 
 
 def spec_kv_release(new_len, seq_len, block_table, ref_count, page_size: int, *, workspace=None, stream=None):
@@ -866,12 +880,12 @@ def spec_kv_release(new_len, seq_len, block_table, ref_count, page_size: int, *,
     ``block_table`` int32 [B, max_pages] (negative: no page), ``ref_count``
     int32 [num_pages]; all updated in place.  Returns the workspace (its error
     word is read by :func:`kv_pages_read_error`)."""
-    dev, dims = _pages(block_table, ref_count, page_size, seq_len, new_len, workspace)
+    dev, dims, nbytes = _pages(block_table, ref_count, page_size, seq_len, new_len, workspace)
     if new_len is not None:
         _int32(new_len, "new_len", (dims.B,))
     lib = library()
     with _Launch(dev, stream) as s:
-        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        workspace = _scratch(workspace, nbytes, dev)
         _check(lib.spec_kv_release(_at(new_len), seq_len.data_ptr(), block_table.data_ptr(), ref_count.data_ptr(), dims,
                                    workspace.data_ptr(), workspace.numel(), s))
     return workspace
@@ -880,14 +894,14 @@ def spec_kv_release(new_len, seq_len, block_table, ref_count, page_size: int, *,
 def spec_kv_fork(src, dst, seq_len, block_table, ref_count, page_size: int, *, workspace=None, stream=None):
     """Sequence ``dst[i]`` (holding no page) becomes a copy of ``src[i]`` that
     shares its pages; ``src`` and ``dst`` int32 [n].  Returns the workspace."""
-    dev, dims = _pages(block_table, ref_count, page_size, seq_len, src, dst, workspace)
+    dev, dims, nbytes = _pages(block_table, ref_count, page_size, seq_len, src, dst, workspace)
     if src.dim() != 1:
         raise ValueError("src and dst must be [n]")
     _int32(src, "src", src.shape)
     _int32(dst, "dst", src.shape)
     lib = library()
     with _Launch(dev, stream) as s:
-        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        workspace = _scratch(workspace, nbytes, dev)
         _check(lib.spec_kv_fork(src.data_ptr(), dst.data_ptr(), src.shape[0], seq_len.data_ptr(),
                                 block_table.data_ptr(), ref_count.data_ptr(), dims, workspace.data_ptr(),
                                 workspace.numel(), s))
@@ -898,13 +912,13 @@ def spec_kv_reserve(num_new, seq_len, block_table, ref_count, pool, *, workspace
     """Make the ``num_new`` (int32 [B]) positions behind ``seq_len`` writable:
     new pages where the table holds none, own copies of shared ones.  ``pool``
     [layers, num_pages, page_size, E].  Returns the workspace."""
-    dev, dims = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, seq_len, num_new, pool,
+    dev, dims, nbytes = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, seq_len, num_new, pool,
                        workspace)
     layers, entry = _pool_planes(pool, dims.num_pages)
     _int32(num_new, "num_new", (dims.B,))
     lib = library()
     with _Launch(dev, stream) as s:
-        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        workspace = _scratch(workspace, nbytes, dev)
         _check(lib.spec_kv_reserve(num_new.data_ptr(), seq_len.data_ptr(), block_table.data_ptr(),
                                    ref_count.data_ptr(), pool.data_ptr(), layers, entry, dims, workspace.data_ptr(),
                                    workspace.numel(), s))
@@ -915,17 +929,29 @@ def spec_kv_compact(block_table, ref_count, pool, *, out_num_live=None, workspac
     """Move the live pages to the front of ``pool`` [layers, num_pages,
     page_size, E]; ``out_num_live`` int32 [1] receives how many there are.
     Returns the workspace."""
-    dev, dims = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, None, pool, out_num_live,
+    dev, dims, nbytes = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, None, pool, out_num_live,
                        workspace)
     layers, entry = _pool_planes(pool, dims.num_pages)
     if out_num_live is not None:
         _int32(out_num_live, "out_num_live", (1,))
     lib = library()
     with _Launch(dev, stream) as s:
-        workspace = _scratch(workspace, lib.spec_kv_pages_workspace_bytes(dims), dev)
+        workspace = _scratch(workspace, nbytes, dev)
         _check(lib.spec_kv_compact(block_table.data_ptr(), ref_count.data_ptr(), pool.data_ptr(), layers, entry,
                                    _at(out_num_live), dims, workspace.data_ptr(), workspace.numel(), s))
     return workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _path_plan(path_shape, pool_shape, table_shape, element):
+    if len(path_shape) != 2 or len(table_shape) != 2:
+        raise ValueError("path must be [B][N] and block_table [B][max_pages]")
+    if len(pool_shape) != 4:
+        raise ValueError("pool must be contiguous [layers][num_pages][page_size][E]")
+    B, N = path_shape
+    layers, num_pages, page_size, E = pool_shape
+    dims = SpecKvDims(B, N, layers, page_size, num_pages, table_shape[1], E * element)
+    return dims, int(library().spec_kv_path_workspace_bytes(dims))
 
 
 def kv_path_workspace(B: int, device="cuda") -> torch.Tensor:
@@ -941,27 +967,24 @@ def spec_kv_commit_path(num_accepted, path, seq_len, block_table, pool, staged=N
     from positions ``seq_len`` + node of the pool [layers, num_pages,
     page_size, E]; ``seq_len`` advances.  Returns the workspace (its error word
     is read by :func:`kv_pages_read_error`)."""
-    if path.dim() != 2 or block_table.dim() != 2:
-        raise ValueError("path must be [B][N] and block_table [B][max_pages]")
-    if pool.dim() != 4 or not pool.is_contiguous():
-        raise ValueError("pool must be contiguous [layers][num_pages][page_size][E]")
-    B, N = path.shape
-    layers, num_pages, page_size, E = pool.shape
+    dims, nbytes = _path_plan(path.shape, pool.shape, block_table.shape, pool.element_size())
     dev = _one_device(pool, "pool", num_accepted, path, seq_len, block_table, staged, workspace)
-    _int32(path, "path", (B, N))
+    if not pool.is_contiguous():
+        raise ValueError("pool must be contiguous [layers][num_pages][page_size][E]")
+    B = dims.B
+    _int32(path, "path", path.shape)
     _int32(num_accepted, "num_accepted", (B,))
     _int32(seq_len, "seq_len", (B,))
-    _int32(block_table, "block_table", (B, block_table.shape[1]))
-    if staged is not None and (staged.dtype != pool.dtype or staged.shape != (layers, B, N, E)
+    _int32(block_table, "block_table", (B, dims.max_pages))
+    if staged is not None and (staged.dtype != pool.dtype
+                               or staged.shape != (dims.layers, B, dims.S, pool.shape[3])
                                or not staged.is_contiguous()):
-        raise ValueError(f"staged must be contiguous {pool.dtype} [{layers}][{B}][{N}][{E}]")
-    dims = SpecKvDims(B, N, layers, page_size, num_pages, block_table.shape[1], E * pool.element_size())
-    lib = library()
+        raise ValueError(f"staged must be contiguous {pool.dtype} [{dims.layers}][{B}][{dims.S}][{pool.shape[3]}]")
     with _Launch(dev, stream) as s:
-        workspace = _scratch(workspace, lib.spec_kv_path_workspace_bytes(dims), dev)
-        _check(lib.spec_kv_commit_path(num_accepted.data_ptr(), path.data_ptr(), seq_len.data_ptr(),
-                                       block_table.data_ptr(), _at(staged), pool.data_ptr(), dims,
-                                       workspace.data_ptr(), workspace.numel(), s))
+        workspace = _scratch(workspace, nbytes, dev)
+        _check(library().spec_kv_commit_path(num_accepted.data_ptr(), path.data_ptr(), seq_len.data_ptr(),
+                                             block_table.data_ptr(), _at(staged), pool.data_ptr(), dims,
+                                             workspace.data_ptr(), workspace.numel(), s))
     return workspace
 
 

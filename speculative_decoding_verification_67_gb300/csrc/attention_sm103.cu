@@ -63,25 +63,34 @@ constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
 constexpr int kItemUnits = 2;        // an item's start and end, in blocks
 constexpr int kMaxTree = 256;
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSplit = 4;        // CTAs that share the rows of one join
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // log2 of the largest weight before O is rescaled
 
-// a / b for non-negative values, in 32 bits where they fit (most do; the 64-bit division takes several hundred clocks).
+// a / b for non-negative values, in 32 bits where they fit (most do; the
+// 64-bit division takes several hundred clocks).
+__device__ __noinline__ long long quot_64(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long quot(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
+  return quot_64(a, b);
 }
 
-// The units before CTA c's share: `q` each, the first `r` CTAs one more.
+// The units before CTA c's share: `q` each, the first `r` CTAs one more; none behind the total.
 struct Shares {
-  long long q;
+  long long q, total;
   int r;
-  __device__ __forceinline__ long long before(int c) const { return q * c + min(c, r); }
+  // the CTA that has unit u
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long wide = r * (q + 1);
+    return static_cast<int>(u < wide ? quot(u, q + 1) : r + quot(u - wide, q));
+  }
+  __device__ __forceinline__ long long before(int c) const { return min(total, q * c + min(c, r)); }
 };
 
-__device__ __forceinline__ Shares shares_of(long long total, int grid) {
+// At least `least` units each: a piece of an item costs its rows' way through memory once more.
+__device__ __forceinline__ Shares shares_of(long long total, int grid, int least) {
+  if (total < static_cast<long long>(grid) * least) grid = max(1, static_cast<int>(total) / least);
   Shares s;
+  s.total = total;
   s.q = quot(total, grid);
   s.r = static_cast<int>(total - s.q * grid);
   return s;
@@ -111,6 +120,8 @@ struct AttnArgs {
   int B, S, heads, kv_heads, G, page_size, num_pages, max_pages, total_q, total_k;
   int tile_tokens;        // whole tokens in a row tile
   int box;                // rows of one page box (a divisor of the page and of a block), or 0: row by row
+  int least;              // units of the smallest share
+  int join_split;         // CTAs that share the rows of one join
   long long k_stride, v_stride;
   // workspace
   int* ctrl;
@@ -170,7 +181,7 @@ __device__ __forceinline__ int item_blocks(const AttnArgs& a, const Seq& s, int 
 }
 
 // sum over i < n of floor((x i + y) / m), by the Euclidean recursion.
-__device__ long long floor_sum(long long n, long long m, long long x, long long y) {
+__device__ __noinline__ long long floor_sum(long long n, long long m, long long x, long long y) {
   long long sum = 0;
   while (n > 0) {
     if (x >= m) {
@@ -196,7 +207,7 @@ __device__ long long floor_sum(long long n, long long m, long long x, long long 
 
 // Units (blocks and kItemUnits each) of the first t items of one head of a sequence.
 template <bool kPaged>
-__device__ long long head_units(const AttnArgs& a, const Seq& s, int t) {
+__device__ __noinline__ long long head_units(const AttnArgs& a, const Seq& s, int t) {
   long long sum = static_cast<long long>(t) * kItemUnits;
   if (kPaged) return sum + static_cast<long long>(t) * item_blocks<kPaged>(a, s, 0);
   const int span = a.tile_tokens * 2;
@@ -404,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cta = blockIdx.x;
   const int grid = gridDim.x;
 
-  sv::griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
       sv::mbar_init(&sh.full[i], kPaged ? 32 * kCopyWarps : 1);
@@ -421,7 +431,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     sv::mbar_init(&sh.done, 1);
     sv::fence_barrier_init();
     sh.abort = 0;
-    a.cuts[cta].active = 0;
   }
   if (warp == kMmaWarp) {
     sv::tmem_alloc(&sh.tmem, Sh::kTmemCols);
@@ -432,6 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     sv::prefetch_tensor_map(&map_k);
     if (!kPaged) sv::prefetch_tensor_map(&map_v);
   }
+
+  // up to here nothing of the caller's was touched: what came before on the stream may still run
+  sv::griddep_wait();
+  sv::griddep_launch_dependents();
+  if (tid == 0) a.cuts[cta].active = 0;
 
   // ---- this CTA's share of the units: a scan over the sequences
   long long total = 0;
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pass == 0 && b0 + kThreads < a.B) continue;  // the total is not known yet
       if (pass == 0) total = seen;
       if (pass == 0 && a.B > kThreads) break;          // find the start in a second pass
-      const long long u0 = shares_of(total, grid).before(cta);
+      const long long u0 = shares_of(total, grid, a.least).before(cta);
       if (units > 0 && before <= u0 && u0 < before + units) {
         const long long per_head = quot(units, a.kv_heads), kvh = quot(u0 - before, per_head);
         const long long r = u0 - before - kvh * per_head;
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.B <= kThreads) break;
   }
   if (tid == 0) {
-    sh.shares = shares_of(total, grid);
+    sh.shares = shares_of(total, grid, a.least);
     sh.u0 = sh.shares.before(cta);
     sh.u1 = sh.shares.before(cta + 1);
   }
@@ -1109,40 +1123,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial rows of every item that was cut, zeroes the rows of
 // sequences found bad, and publishes the error word.  CTA (c, y) takes every
-// kJoinSplit-th group of rows of the item whose first cut CTA c begins with.
-// A few partial rows (at most one item per CTA of the main kernel) of L2
-// traffic: bound by latency.
+// join_split-th group of rows of the item whose first cut CTA c begins with; a
+// warp takes a row: lane p weighs piece p, then every lane adds up its columns,
+// several pieces' loads in flight.  At most one item per CTA of the main
+// kernel is cut: a few MB of L2 traffic, bound by latency.
 template <typename T, int D, bool kPaged>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int main_grid) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
   constexpr int kNT = kTiles<kPaged>, kE = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sv::griddep_wait();
+  sv::griddep_launch_dependents();
   const Cut cut = a.cuts[blockIdx.x];
   if (cut.active && !(kPaged && a.bad[cut.b])) {
     int err;
     const Seq s = get_seq<kPaged>(a, cut.b, err);
     const int tok0 = cut.tile * a.tile_tokens * kNT;
-    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < kNT * kBlock; r += kJoinSplit * (kJoinThreads / 32)) {
-      const int sub = r / kBlock, in = r % kBlock, tok = tok0 + sub * a.tile_tokens + in / a.G;
+    const int first = cut.first, last = cut.shares.owner(cut.start + kItemUnits + cut.n - 1);
+    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < kNT * kBlock; r += a.join_split * (kJoinThreads / 32)) {
+      const int in = r % kBlock, tok = tok0 + r / kBlock * a.tile_tokens + in / a.G;
       if (in >= a.tile_tokens * a.G || tok >= s.Lq) continue;
+      // the first piece is its CTA's last segment, the others are their CTAs' first
+      auto place = [&](int p) {
+        return (static_cast<long long>(p) * 2 + (p == first ? 1 : 0)) * (kNT * kBlock) + r;
+      };
       float o[kE], ref = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) o[e] = 0.f;
-      for (int p = cut.first; p < main_grid; ++p) {
-        const long long from = cut.shares.before(p);
-        if (from == cut.shares.before(p + 1)) break;
-        if (p > cut.first && from - cut.start - kItemUnits >= cut.n) break;
-        const long long at = (static_cast<long long>(p) * 2 + (p == cut.first ? 1 : 0)) * (kNT * kBlock) + r;
-        const float2 ml = a.part_ml[at];
-        if (ml.x == -INFINITY) continue;  // this piece saw no key
-        const float top = fmaxf(ref, ml.x);
-        const float f = ref == -INFINITY ? 0.f : exp2_approx(ref - top), g = exp2_approx(ml.x - top);
-        sum = sum * f + ml.y * g;
-        ref = top;
+      for (int p0 = first; p0 <= last; p0 += 32) {  // (one round for up to 32 pieces)
+        const float2 ml = p0 + lane <= last ? a.part_ml[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float x = a.part_o[at * D + lane * kE + e];
-          o[e] = (f == 0.f ? 0.f : o[e] * f) + (g == 0.f ? 0.f : x * g);
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, ref);
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
+        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
+        ref = top;
+        sum = keep == 0.f ? 0.f : sum * keep;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
+        const float l = f == 0.f ? 0.f : ml.y * f;
+        const int n = min(32, last - p0 + 1);
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+          const float g = __shfl_sync(0xffffffffu, f, p);
+          sum += __shfl_sync(0xffffffffu, l, p);
+          const float* from = a.part_o + place(p0 + p) * D + lane * kE;
+          float x[kE];
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(from + e);
+            x[e] = v.x;
+            x[e + 1] = v.y;
+          }
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o[e] += g == 0.f ? 0.f : x[e] * g;
         }
       }
       const bool none = sum == 0.f;
@@ -1155,7 +1189,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     }
   }
   if (kPaged) {
-    for (int b = blockIdx.x * kJoinSplit + blockIdx.y; b < a.B; b += gridDim.x * kJoinSplit) {
+    for (int b = blockIdx.x * a.join_split + blockIdx.y; b < a.B; b += gridDim.x * a.join_split) {
       if (!a.bad[b]) continue;
       const int n = a.len_k ? a.len_k[b] : a.S;
       const long long rows = static_cast<long long>(n < 0 || n > a.S ? a.S : n) * a.heads;
@@ -1276,9 +1310,19 @@ spec_status launch(const AttnArgs& a, const CUtensorMap (&maps)[3], const sv::De
     done[dev.device] = true;
   }
   const int grid = dev.sm_count < kMaxGrid ? dev.sm_count : kMaxGrid;
-  attn_kernel<T, D, kPaged><<<grid, kThreads, kBytes, s>>>(a, maps[0], maps[1], maps[2]);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
-  if (sv::launch_dependent(attn_join_kernel<T, D, kPaged>, dim3(grid, kJoinSplit), dim3(kJoinThreads), s, a, grid) !=
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_kernel<T, D, kPaged>, a, maps[0], maps[1], maps[2]) != cudaSuccess)
+    return SPEC_ERR_CUDA;
+  if (sv::launch_dependent(attn_join_kernel<T, D, kPaged>, dim3(grid, a.join_split), dim3(kJoinThreads), s, a) !=
       cudaSuccess)
     return SPEC_ERR_CUDA;
   return SPEC_OK;
@@ -1352,6 +1396,9 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens))
     return SPEC_ERR_CUDA;
   // Boxes of at least eight rows; below that one copy of 16 bytes per thread is faster.
+  // Up to 16 rows (one token) a piece is next to nothing to join.
+  a.least = dims.S * a.G <= 16 ? 1 : 4;
+  a.join_split = dims.S * a.G <= 16 ? 1 : 4;
   a.box = kBlock;
   while (a.box >= 8 && dims.page_size % a.box != 0) a.box /= 2;
   if (a.box < 8) a.box = 0;
@@ -1395,6 +1442,8 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
   a.k_stride = dims.k_stride;
   a.v_stride = dims.v_stride;
   a.tile_tokens = kBlock / a.G;
+  a.least = 6;
+  a.join_split = 4;
   CUtensorMap maps[3];
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, dims.total_q, dims.q_stride, a.G,
                      a.tile_tokens) ||
