@@ -270,6 +270,7 @@ struct Sync {
 struct Exchange {
   float ref[2][2][kBlock];        // [segment parity][tile][row]
   float sum[2][2][kBlock];
+  uint4 rows[8][128];             // [softmax warp] 64 bytes of each of its rows, on their way out
 };
 
 struct TreeShared {
@@ -1060,42 +1061,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (joint) wait(&sh.o_full[1], used[1] & 1);
       sv::tc_fence_after_sync();
       if (alive) {
-        const bool mine = row < rows;
-        const long long orow = (static_cast<long long>(s.q0) + i_tok) * a.heads + at.kvh * a.G + row % a.G;
         const bool none = all == 0.f;
         const float inv = whole && !none ? 1.f / all : 1.f;
-        const int prow = kPaged ? row : t * kBlock + row;
+        const int prow = kPaged ? 0 : t * kBlock;
         const uint32_t from = tmem + Sh::kO + t0 * D + lanes;
-#pragma unroll 1
-        for (int d = d0; d < d0 + width; d += 16) {
-          float o[16];
-          sv::tmem_load_16(from + d, o);
-          if (joint) {
-            float o2[16];
-            sv::tmem_load_16(from + D + d, o2);
+        const int row0 = row & ~31;  // the warp's first row
+        // A thread holds a row; the warp passes 64 bytes of each of its rows through shared memory, so that a store
+        // covers whole sectors of eight rows instead of pieces of 32.
+        uint4* stage = ex.rows[warp];
+        const int sub = lane >> 2, piece = lane & 3;  // in a store: row 8 k + sub, 16 bytes
+        int at_row[4];                                // rows of out (whole) or of the partial rows, from the base
+        const long long base_row = whole ? (static_cast<long long>(s.q0) + tok0) * a.heads + at.kvh * a.G : slot + prow;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+        for (int k = 0; k < 4; ++k) {
+          const int r = row0 + 8 * k + sub;
+          at_row[k] = r >= rows ? -1 : (whole ? r / a.G * a.heads + r % a.G : r);
+        }
+        auto put = [&](uint4 v, int c) { stage[lane * 4 + (c ^ (lane >> 1 & 3))] = v; };
+        auto flush = [&](char* base, int pitch) {  // base: the 64 bytes' place in base_row
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 8 * k + sub;
+            const uint4 v = stage[r * 4 + (piece ^ (r >> 1 & 3))];
+            if (at_row[k] >= 0)
+              *reinterpret_cast<uint4*>(base + static_cast<long long>(at_row[k]) * pitch + piece * 16) = v;
           }
-          if (!mine) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + d);
+          __syncwarp();
+        };
+        if (whole) {
+          char* base = reinterpret_cast<char*>(static_cast<T*>(a.out) + base_row * D);
+#pragma unroll 1
+          for (int d = d0; d < d0 + width; d += 32) {
+            float o[32];
+            sv::tmem_load_32(from + d, o);
+            if (joint) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+              for (int h = 0; h < 2; ++h) {
+                float o2[16];
+                sv::tmem_load_16(from + D + d + 16 * h, o2);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  o[16 * h + e] = (f0 == 0.f ? 0.f : o[16 * h + e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = none ? 0u : pack2(o[8 * e + 2 * k] * inv, o[8 * e + 2 * k + 1] * inv, T());
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                w[k] = none ? 0u : pack2(o[8 * c + 2 * k] * inv, o[8 * c + 2 * k + 1] * inv, T());
+              put(make_uint4(w[0], w[1], w[2], w[3]), c);
             }
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (slot + prow) * D + d);
+            flush(base + d * 2, D * 2);
+          }
+        } else {
+          char* base = reinterpret_cast<char*>(a.part_o + base_row * D);
+#pragma unroll 1
+          for (int d = d0; d < d0 + width; d += 16) {
+            float o[16];
+            sv::tmem_load_16(from + d, o);
+            if (joint) {
+              float o2[16];
+              sv::tmem_load_16(from + D + d, o2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 16; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              put(make_uint4(__float_as_uint(o[4 * c]), __float_as_uint(o[4 * c + 1]), __float_as_uint(o[4 * c + 2]),
+                             __float_as_uint(o[4 * c + 3])), c);
+            flush(base + d * 4, D * 4);
           }
         }
-        if (mine && d0 == 0) {
-          if (!whole) a.part_ml[slot + prow] = make_float2(base2, all);
-          else if (a.lse) a.lse[orow] = none ? -INFINITY : (base2 + log2f(all)) * kLn2;
+        if (row < rows && d0 == 0) {
+          if (!whole) a.part_ml[base_row + row] = make_float2(base2, all);
+          else if (a.lse) a.lse[base_row + row / a.G * a.heads + row % a.G] = none ? -INFINITY : (base2 + log2f(all)) * kLn2;
         }
       }
       sv::tc_fence_before_sync();
