@@ -60,7 +60,10 @@ constexpr int kThreads = 384;        // two softmax warpgroups, an MMA warp, thr
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kCopyWarps = 3;        // load warps of the cache form
 constexpr int kMaxGrid = 160;        // CTAs (one per SM); sizes the workspace
-constexpr int kItemUnits = 2;        // an item's start and end, in blocks
+// An item's start and end, in blocks (sets the shares): one 12301-token prompt took 950 us with 2, 915 with 3, 907
+// with 4 and 921 with 6, 16 shorter ones 262, 251, 253 and 270; over the cache, where a block takes less, 2 did best.
+template <bool kPaged>
+constexpr int kItemUnits = kPaged ? 2 : 3;
 constexpr int kMaxTree = 256;
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -208,7 +211,7 @@ __device__ __noinline__ long long floor_sum(long long n, long long m, long long 
 // Units (blocks and kItemUnits each) of the first t items of one head of a sequence.
 template <bool kPaged>
 __device__ __noinline__ long long head_units(const AttnArgs& a, const Seq& s, int t) {
-  long long sum = static_cast<long long>(t) * kItemUnits;
+  long long sum = static_cast<long long>(t) * kItemUnits<kPaged>;
   if (kPaged) return sum + static_cast<long long>(t) * item_blocks<kPaged>(a, s, 0);
   const int span = a.tile_tokens * 2;
   const int full = t < s.tiles ? t : s.tiles - 1;  // tiles whose last token is (i + 1) span - 1
@@ -227,7 +230,7 @@ struct Cursor {
   Seq s;
 
   __device__ void next(const AttnArgs& a) {
-    start += n + kItemUnits;
+    start += n + kItemUnits<kPaged>;
     if (++tile < s.tiles) {
       if (!kPaged) n = item_blocks<kPaged>(a, s, tile);
       return;
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long r = u0 - before - kvh * per_head;
         int lo = 0, hi = s.tiles;  // the last tile that starts at or before r
         if (kPaged) {
-          lo = static_cast<int>(quot(r, item_blocks<kPaged>(a, s, 0) + kItemUnits));
+          lo = static_cast<int>(quot(r, item_blocks<kPaged>(a, s, 0) + kItemUnits<kPaged>));
         } else {
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -557,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (lw < (kPaged ? kCopyWarps : 1)) {
       for (; at.start < u1; at.next(a)) {
-        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
-        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits<kPaged>));
+        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits<kPaged>));
         if (hi <= lo) continue;
         if (kPaged) {
           const int committed = a.staged ? blocks_of(at.s.base) : at.n;  // blocks read from the pool
@@ -730,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       for (; at.start < u1; at.next(a)) {
-        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
-        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+        const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits<kPaged>));
+        const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits<kPaged>));
         const int nb = hi - lo;
         if (nb <= 0) continue;
         await(sh, &sh.q_full, segs & 1);
@@ -809,8 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     for (; at.start < u1; at.next(a)) {
-      const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits));
-      const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits));
+      const int lo = static_cast<int>(max(0ll, u0 - at.start - kItemUnits<kPaged>));
+      const int hi = static_cast<int>(min(static_cast<long long>(at.n), u1 - at.start - kItemUnits<kPaged>));
       const int nb = hi - lo;
       if (nb <= 0) continue;
       const Seq& s = at.s;
@@ -827,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cut.tile = at.tile;
         cut.n = at.n;
         cut.first = cta - 1;  // (every CTA before one with a share has one)
-        cut.active = sh.shares.before(cta - 1) - at.start - kItemUnits <= 0;
+        cut.active = sh.shares.before(cta - 1) - at.start - kItemUnits<kPaged> <= 0;
         a.cuts[cta] = cut;
       }
       if (t == 1 && !both) {
@@ -873,10 +876,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool masked = least < kBlock;
         const bool look = masked && (!kPaged || (s.Lq > 1 && (fresh || !a.staged)));
-        wait(&sh.s_full[t], s_cnt & 1);
-        ++s_cnt;
-        sv::tc_fence_after_sync();
+        auto scored = [&]() {
+          wait(&sh.s_full[t], s_cnt & 1);
+          ++s_cnt;
+          sv::tc_fence_after_sync();
+        };
         unsigned spoil[4] = {0, 0, 0, 0};
+        // Prompts look while the scores are on their way.  (The load before V's in the ring was consumed by the block
+        // before.  Over the cache it may be the other tile's next K, which has landed for sure only with the scores.)
+        if (kPaged) scored();
         if (look) {
           // one row of the V tile per thread; where both tiles read it, each half of the row
           const bool pair = !kPaged && both;
@@ -914,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               spoil[w] &= keys >= 32 * (w + 1) ? 0xffffffffu : (keys <= 32 * w ? 0u : (1u << (keys - 32 * w)) - 1u);
           }
         }
+        if (!kPaged) scored();
         const bool spoils = (spoil[0] | spoil[1] | spoil[2] | spoil[3]) != 0;
         if (first && row == 0) *reinterpret_cast<volatile int*>(&sh.o_set[t]) = spoils;
         // bit c of word w: column 32 w + c is seen
@@ -1179,7 +1188,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     int err;
     const Seq s = get_seq<kPaged>(a, cut.b, err);
     const int tok0 = cut.tile * a.tile_tokens * kNT;
-    const int first = cut.first, last = cut.shares.owner(cut.start + kItemUnits + cut.n - 1);
+    const int first = cut.first, last = cut.shares.owner(cut.start + kItemUnits<kPaged> + cut.n - 1);
     for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < kNT * kBlock; r += a.join_split * (kJoinThreads / 32)) {
       const int in = r % kBlock, tok = tok0 + r / kBlock * a.tile_tokens + in / a.G;
       if (in >= a.tile_tokens * a.G || tok >= s.Lq) continue;
