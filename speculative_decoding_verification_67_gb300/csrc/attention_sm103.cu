@@ -101,11 +101,12 @@ __device__ __forceinline__ Shares shares_of(long long total, int grid, int least
 
 // What a join needs to know of an item that was cut (one record per CTA).
 struct Cut {
-  long long start;         // first unit of the item
-  Shares shares;
   int active;
-  int b, kvh, tile, n;     // the item and its blocks
-  int first;               // the CTA that holds block 0
+  int first;           // the CTA with its first piece
+  int b, tokens;       // the sequence, the item's tokens
+  long long row;       // the row of out of its first token's first head
+  long long end;       // its last unit
+  Shares shares;
 };
 
 struct AttnArgs {
@@ -133,6 +134,12 @@ struct AttnArgs {
   float* part_o;          // [kMaxGrid][2][rows][D]
   float2* part_ml;        // [kMaxGrid][2][rows] (reference in log2, sum)
 };
+
+// Marks a sequence of the cache form (or, b < 0, the call) with error bits.
+__device__ __forceinline__ void report(const AttnArgs& a, int b, int bits) {
+  if (b >= 0) atomicOr(a.bad + b, bits);
+  atomicOr(a.ctrl + sv::kKvCollect, bits);
+}
 
 // One sequence: Lq queries behind `base` keys (packed: negative when there are fewer keys than queries).
 struct Seq {
@@ -210,7 +217,7 @@ __device__ __noinline__ long long floor_sum(long long n, long long m, long long 
 
 // Units (blocks and kItemUnits each) of the first t items of one head of a sequence.
 template <bool kPaged>
-__device__ __noinline__ long long head_units(const AttnArgs& a, const Seq& s, int t) {
+__device__ __noinline__ long long head_units(const AttnArgs& a, const Seq s, int t) {
   long long sum = static_cast<long long>(t) * kItemUnits<kPaged>;
   if (kPaged) return sum + static_cast<long long>(t) * item_blocks<kPaged>(a, s, 0);
   const int span = a.tile_tokens * 2;
@@ -220,6 +227,33 @@ __device__ __noinline__ long long head_units(const AttnArgs& a, const Seq& s, in
   sum += none + floor_sum(full - none, kBlock, span, s.base + static_cast<long long>(none + 1) * span + kBlock - 1);
   if (t == s.tiles) sum += item_blocks<kPaged>(a, s, t - 1);
   return sum;
+}
+
+// The item that has unit u, of sequence s whose units begin at `before`.
+struct Place {
+  int kvh, tile;
+  long long start;  // the item's first unit
+};
+
+template <bool kPaged>
+__device__ __noinline__ Place locate(const AttnArgs& a, const Seq s, long long units, long long before, long long u) {
+  const long long per_head = quot(units, a.kv_heads), kvh = quot(u - before, per_head);
+  const long long r = u - before - kvh * per_head;
+  int lo = 0, hi = s.tiles;  // the last tile that starts at or before r
+  if (kPaged) {
+    lo = static_cast<int>(quot(r, item_blocks<kPaged>(a, s, 0) + kItemUnits<kPaged>));
+  } else {
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (head_units<kPaged>(a, s, mid) <= r) lo = mid;
+      else hi = mid;
+    }
+  }
+  Place p;
+  p.kvh = static_cast<int>(kvh);
+  p.tile = lo;
+  p.start = u - r + (lo ? head_units<kPaged>(a, s, lo) : 0);
+  return p;
 }
 
 // A place in the list of items.
@@ -263,10 +297,10 @@ struct Sync {
   int abort;
   int o_set[2];             // the softmax warps have written O themselves
   unsigned spoiled[2][2][4];
-  long long u0, u1, start;
   Shares shares;
-  int b, kvh, tile;
-  Seq seq;
+  int at_b, at_kvh, at_tile;
+  long long at_start;
+  Seq at_seq;
   long long scan[kThreads / 32];
 };
 
@@ -399,6 +433,89 @@ __device__ const T* value_row(const AttnArgs& a, const Seq& s, int b, int kvh, b
   return base + row * entry + static_cast<long long>(a.kv_heads + kvh) * D;
 }
 
+// Where the CTA's share begins, into shared memory.  (Functions of their own,
+// so that what they need does not weigh on the registers of the loops.)
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+template <bool kPaged>
+__device__ __forceinline__ void begin_at(const AttnArgs& a, Sync& sh, const Seq s, int b, long long units,
+                                         long long before, long long u) {
+  const Place p = locate<kPaged>(a, s, units, before, u);
+  sh.at_b = b;
+  sh.at_kvh = p.kvh;
+  sh.at_tile = p.tile;
+  sh.at_start = p.start;
+  sh.at_seq = s;
+}
+
+// Up to 32 sequences: one warp.
+template <bool kPaged>
+__device__ __noinline__ void scan_few(const AttnArgs& a, Sync& sh, int grid, int cta) {
+  const int lane = threadIdx.x & 31;
+  Seq s;
+  s.tiles = 0;
+  long long units = 0;
+  if (lane < a.B) {
+    int err;
+    s = get_seq<kPaged>(a, lane, err);
+    if (s.tiles > 0) units = head_units<kPaged>(a, s, s.tiles) * a.kv_heads;
+    if (err && cta == 0) report(a, kPaged ? lane : -1, err);
+  }
+  const long long x = warp_scan(units, lane);
+  const Shares shares = shares_of(__shfl_sync(0xffffffffu, x, 31), grid, a.least);
+  const long long u = shares.before(cta);
+  if (lane == 0) sh.shares = shares;
+  if (units > 0 && x - units <= u && u < x) begin_at<kPaged>(a, sh, s, lane, units, x - units, u);
+}
+
+// More: the whole CTA, in two passes where a thread has more than one sequence.
+template <bool kPaged>
+__device__ __noinline__ void scan_many(const AttnArgs& a, Sync& sh, int grid, int cta) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long long total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long seen = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long units = 0;
+      Seq s;
+      s.tiles = 0;
+      if (b < a.B) {
+        int err;
+        s = get_seq<kPaged>(a, b, err);
+        if (s.tiles > 0) units = head_units<kPaged>(a, s, s.tiles) * a.kv_heads;
+        if (err && pass == 0 && cta == 0) report(a, kPaged ? b : -1, err);
+      }
+      const long long x = warp_scan(units, lane);
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = x;
+      __syncthreads();
+      long long before = seen, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh.scan[w];
+        sum += sh.scan[w];
+      }
+      before += x - units;
+      seen += sum;
+      if (pass == 0 && b0 + kThreads < a.B) continue;  // the total is not known yet
+      if (pass == 0) total = seen;
+      if (pass == 0 && a.B > kThreads) break;          // find the start in a second pass
+      const long long u = shares_of(total, grid, a.least).before(cta);
+      if (units > 0 && before <= u && u < before + units) begin_at<kPaged>(a, sh, s, b, units, before, u);
+    }
+    if (a.B <= kThreads) break;
+  }
+  if (tid == 0) sh.shares = shares_of(total, grid, a.least);
+}
+
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -452,92 +569,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) a.cuts[cta].active = 0;
 
   // ---- this CTA's share of the units: a scan over the sequences
-  long long total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long seen = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      long long units = 0;
-      Seq s;
-      s.tiles = 0;
-      if (b < a.B) {
-        int err;
-        s = get_seq<kPaged>(a, b, err);
-        if (s.tiles > 0) units = head_units<kPaged>(a, s, s.tiles) * a.kv_heads;
-        if (err && pass == 0 && cta == 0) atomicOr(kPaged ? a.bad + b : a.ctrl + sv::kKvCollect, err);
-      }
-      long long x = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) sh.scan[warp] = x;
-      __syncthreads();
-      long long before = seen, sum = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sh.scan[w];
-        sum += sh.scan[w];
-      }
-      before += x - units;
-      seen += sum;
-      if (pass == 0 && b0 + kThreads < a.B) continue;  // the total is not known yet
-      if (pass == 0) total = seen;
-      if (pass == 0 && a.B > kThreads) break;          // find the start in a second pass
-      const long long u0 = shares_of(total, grid, a.least).before(cta);
-      if (units > 0 && before <= u0 && u0 < before + units) {
-        const long long per_head = quot(units, a.kv_heads), kvh = quot(u0 - before, per_head);
-        const long long r = u0 - before - kvh * per_head;
-        int lo = 0, hi = s.tiles;  // the last tile that starts at or before r
-        if (kPaged) {
-          lo = static_cast<int>(quot(r, item_blocks<kPaged>(a, s, 0) + kItemUnits<kPaged>));
-        } else {
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (head_units<kPaged>(a, s, mid) <= r) lo = mid;
-            else hi = mid;
-          }
-        }
-        sh.b = b;
-        sh.kvh = static_cast<int>(kvh);
-        sh.tile = lo;
-        sh.seq = s;
-        sh.start = u0 - r + (lo ? head_units<kPaged>(a, s, lo) : 0);
-      }
-    }
-    if (a.B <= kThreads) break;
-  }
-  if (tid == 0) {
-    sh.shares = shares_of(total, grid, a.least);
-    sh.u0 = sh.shares.before(cta);
-    sh.u1 = sh.shares.before(cta + 1);
-  }
+  if (a.B > 32) scan_many<kPaged>(a, sh, grid, cta);
+  else if (warp == 0) scan_few<kPaged>(a, sh, grid, cta);
   if (kPaged && a.parents) {  // trees are checked once per sequence
     for (int b = cta; b < a.B; b += gridDim.x) {
       int err;
       const Seq s = get_seq<kPaged>(a, b, err);
       for (int i = tid; i < s.Lq; i += kThreads) {
         const int p = a.parents[static_cast<long long>(b) * a.S + i];
-        if (i == 0 ? p != -1 : (p < 0 || p >= i)) atomicOr(a.bad + b, SPEC_ATTN_DEVERR_TREE);
+        if (i == 0 ? p != -1 : (p < 0 || p >= i)) report(a, b, SPEC_ATTN_DEVERR_TREE);
       }
     }
   }
   sv::tc_fence_before_sync();
   __syncthreads();
   sv::tc_fence_after_sync();
-  const long long u0 = sh.u0, u1 = sh.u1;
   const uint32_t tmem = sh.tmem;
-
+  const long long u0 = sh.shares.before(cta), u1 = sh.shares.before(cta + 1);
   Cursor<kPaged> at = {};
   at.start = u1;  // no share: nothing to walk
   if (u0 < u1) {
-    at.b = sh.b;
-    at.kvh = sh.kvh;
-    at.tile = sh.tile;
-    at.start = sh.start;
-    at.s = sh.seq;
+    at.b = sh.at_b;
+    at.kvh = sh.at_kvh;
+    at.tile = sh.at_tile;
+    at.start = sh.at_start;
+    at.s = sh.at_seq;
     at.n = item_blocks<kPaged>(a, at.s, at.tile);
   }
 
@@ -578,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto row_at = [&](int p) {  // the pool's row of a position
             const int col = p / a.page_size, page = table[col];
             if (page >= 0 && page < a.num_pages) return page * a.page_size + (p - col * a.page_size);
-            atomicOr(a.bad + at.b, SPEC_ATTN_DEVERR_PAGE);
+            report(a, at.b, SPEC_ATTN_DEVERR_PAGE);
             return -1;
           };
           auto rows_of = [&](int j, int (&r)[kEach]) {
@@ -641,9 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             copies_arrive(&sh.full[slot]);
           };
+          if (segs == 0 && lw == 0 && lane == 0) load_q();  // (later ones wait for the last item's products)
+          __syncwarp();
           rows_of(lo, r0);
           copy(lo, r0, at.kvh);
-          if (lw == 0 && lane == 0) load_q();
+          if (segs > 0 && lw == 0 && lane == 0) load_q();
           __syncwarp();
           for (int j = lo; j < hi; ++j) {
             if (j + 1 < hi) {
@@ -823,14 +881,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool both = kPaged ? nb > 1 : s.Lq - item_tok > a.tile_tokens;  // the second score tile is in use
       if (tid == 0 && lo > 0) {
         Cut cut;
-        cut.start = at.start;
-        cut.shares = sh.shares;
-        cut.b = at.b;
-        cut.kvh = at.kvh;
-        cut.tile = at.tile;
-        cut.n = at.n;
         cut.first = cta - 1;  // (every CTA before one with a share has one)
         cut.active = sh.shares.before(cta - 1) - at.start - kItemUnits<kPaged> <= 0;
+        cut.end = at.start + kItemUnits<kPaged> + at.n - 1;
+        cut.shares = sh.shares;
+        cut.b = at.b;
+        cut.tokens = min(a.tile_tokens * kNT, s.Lq - item_tok);
+        cut.row = (static_cast<long long>(s.q0) + item_tok) * a.heads + at.kvh * a.G;
         a.cuts[cta] = cut;
       }
       if (t == 1 && !both) {
@@ -1098,7 +1155,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         };
-        if (whole) {
+        if (kPaged && rows <= 16) {  // few rows: each thread its own
+          const long long mine = base_row + (whole ? row / a.G * a.heads + row % a.G : row);
+#pragma unroll 1
+          for (int d = d0; d < d0 + width; d += 32) {
+            float o[32];
+            sv::tmem_load_32(from + d, o);
+            if (joint) {
+              float o2[32];
+              sv::tmem_load_32(from + D + d, o2);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+            }
+            if (row >= rows) continue;
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + mine * D + d);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = none ? 0u : pack2(o[8 * c + 2 * k] * inv, o[8 * c + 2 * k + 1] * inv, T());
+                dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + mine * D + d);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            }
+          }
+        } else if (whole) {
           char* base = reinterpret_cast<char*>(static_cast<T*>(a.out) + base_row * D);
 #pragma unroll 1
           for (int d = d0; d < d0 + width; d += 32) {
@@ -1168,101 +1254,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   sv::tc_fence_after_sync();
   if (warp == kMmaWarp) sv::tmem_dealloc(tmem, Sh::kTmemCols);
-  if (tid == 0 && sh.abort) atomicOr(a.ctrl + sv::kKvCollect, SPEC_ATTN_DEVERR_TIMEOUT);
+  if (tid == 0 && sh.abort) report(a, -1, SPEC_ATTN_DEVERR_TIMEOUT);
 }
 
 // Joins the partial rows of every item that was cut, zeroes the rows of
 // sequences found bad, and publishes the error word.  CTA (c, y) takes every
 // join_split-th group of rows of the item whose first cut CTA c begins with; a
-// warp takes a row: lane p weighs piece p, then every lane adds up its columns,
-// several pieces' loads in flight.  At most one item per CTA of the main
-// kernel is cut: a few MB of L2 traffic, bound by latency.
+// warp takes a row: lane p weighs piece p while the pieces' columns are on their
+// way.  At most one item per CTA of the main kernel is cut: a few MB of L2
+// traffic, bound by two dependent loads (the record, then all the rest).
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  constexpr int kNT = kTiles<kPaged>, kE = D / 32;
+  constexpr int kNT = kTiles<kPaged>, kE = D / 32, kWarps = kJoinThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sv::griddep_wait();
   sv::griddep_launch_dependents();
   const Cut cut = a.cuts[blockIdx.x];
-  if (cut.active && !(kPaged && a.bad[cut.b])) {
-    int err;
-    const Seq s = get_seq<kPaged>(a, cut.b, err);
-    const int tok0 = cut.tile * a.tile_tokens * kNT;
-    const int first = cut.first, last = cut.shares.owner(cut.start + kItemUnits<kPaged> + cut.n - 1);
-    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < kNT * kBlock; r += a.join_split * (kJoinThreads / 32)) {
-      const int in = r % kBlock, tok = tok0 + r / kBlock * a.tile_tokens + in / a.G;
-      if (in >= a.tile_tokens * a.G || tok >= s.Lq) continue;
-      // the first piece is its CTA's last segment, the others are their CTAs' first
-      auto place = [&](int p) {
-        return (static_cast<long long>(p) * 2 + (p == first ? 1 : 0)) * (kNT * kBlock) + r;
-      };
-      float o[kE], ref = -INFINITY, sum = 0.f;
+  const int errors = a.ctrl[sv::kKvCollect];  // (the main kernel has set them all)
+  const int rows = cut.active ? cut.tokens * a.G : 0;
+  const int last = cut.active ? cut.shares.owner(cut.end) : 0;  // the CTA with the last piece
+  for (int i = blockIdx.y * kWarps + warp; i < rows; i += a.join_split * kWarps) {
+    if (kPaged && errors && a.bad[cut.b]) break;
+    const int tok = i / a.G, g = i % a.G, sub = tok / a.tile_tokens;
+    const int r = sub * kBlock + (tok - sub * a.tile_tokens) * a.G + g;
+    // the first piece is its CTA's last segment, the others are their CTAs' first
+    auto place = [&](int p) {
+      return (static_cast<long long>(p) * 2 + (p == cut.first ? 1 : 0)) * (kNT * kBlock) + r;
+    };
+    float o[kE], ref = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] = 0.f;
-      for (int p0 = first; p0 <= last; p0 += 32) {  // (one round for up to 32 pieces)
-        const float2 ml = p0 + lane <= last ? a.part_ml[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
-        float top = ml.x;
+    for (int e = 0; e < kE; ++e) o[e] = 0.f;
+    for (int p0 = cut.first; p0 <= last; p0 += 32) {  // (one round for up to 32 pieces)
+      const float2 ml = p0 + lane <= last ? a.part_ml[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
+      constexpr int kAhead = 8;
+      float x[kAhead][kE];
+      auto fetch = [&](int q0) {
 #pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        top = fmaxf(top, ref);
-        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
-        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
-        ref = top;
-        sum = keep == 0.f ? 0.f : sum * keep;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
-        const float l = f == 0.f ? 0.f : ml.y * f;
-        const int n = min(32, last - p0 + 1);
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
-          const float g = __shfl_sync(0xffffffffu, f, p);
-          sum += __shfl_sync(0xffffffffu, l, p);
-          const float* from = a.part_o + place(p0 + p) * D + lane * kE;
-          float x[kE];
+        for (int q = 0; q < kAhead; ++q) {
+          if (q0 + q > last) continue;
+          const float* from = a.part_o + place(q0 + q) * D + lane * kE;
 #pragma unroll
           for (int e = 0; e < kE; e += 2) {
             const float2 v = *reinterpret_cast<const float2*>(from + e);
-            x[e] = v.x;
-            x[e + 1] = v.y;
+            x[q][e] = v.x;
+            x[q][e + 1] = v.y;
           }
+        }
+      };
+      fetch(p0);
+      float top = ml.x;
 #pragma unroll
-          for (int e = 0; e < kE; ++e) o[e] += g == 0.f ? 0.f : x[e] * g;
+      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      top = fmaxf(top, ref);
+      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
+      const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
+      ref = top;
+      sum = keep == 0.f ? 0.f : sum * keep;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
+      const float l = f == 0.f ? 0.f : ml.y * f;
+      const int n = min(32, last - p0 + 1);
+      for (int p = 0; p < n; p += kAhead) {
+        if (p > 0) fetch(p0 + p);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          const float w = __shfl_sync(0xffffffffu, f, (p + q) & 31);
+          sum += __shfl_sync(0xffffffffu, l, (p + q) & 31);  // (0 behind the last piece)
+          if (w != 0.f) {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] += x[q][e] * w;
+          }
         }
       }
-      const bool none = sum == 0.f;
-      const float inv = none ? 0.f : 1.f / sum;
-      const long long orow = (static_cast<long long>(s.q0) + tok) * a.heads + cut.kvh * a.G + in % a.G;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + orow * D + lane * kE);
-#pragma unroll
-      for (int e = 0; e < kE; e += 2) dst[e / 2] = none ? 0u : pack2(o[e] * inv, o[e + 1] * inv, T());
-      if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : (ref + log2f(sum)) * kLn2;
     }
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    const long long orow = cut.row + static_cast<long long>(tok) * a.heads + g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + orow * D + lane * kE);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) dst[e / 2] = none ? 0u : pack2(o[e] * inv, o[e + 1] * inv, T());
+    if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  }
+  if (errors == 0) {  // (the same answer in every CTA)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.ctrl[sv::kKvErr] = 0;
+    return;
   }
   if (kPaged) {
     for (int b = blockIdx.x * a.join_split + blockIdx.y; b < a.B; b += gridDim.x * a.join_split) {
       if (!a.bad[b]) continue;
       const int n = a.len_k ? a.len_k[b] : a.S;
-      const long long rows = static_cast<long long>(n < 0 || n > a.S ? a.S : n) * a.heads;
+      const long long count = static_cast<long long>(n < 0 || n > a.S ? a.S : n) * a.heads;
       uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<long long>(b) * a.S * a.heads * D);
-      for (long long i = threadIdx.x; i < rows * D / 8; i += kJoinThreads) dst[i] = make_uint4(0, 0, 0, 0);
+      for (long long i = threadIdx.x; i < count * D / 8; i += kJoinThreads) dst[i] = make_uint4(0, 0, 0, 0);
       if (a.lse)
-        for (long long i = threadIdx.x; i < rows; i += kJoinThreads)
+        for (long long i = threadIdx.x; i < count; i += kJoinThreads)
           a.lse[static_cast<long long>(b) * a.S * a.heads + i] = -INFINITY;
     }
   }
+  // the last CTA leaves the marks ready for the next call
   __shared__ int s_last;
   __syncthreads();
   if (threadIdx.x == 0) s_last = sv::kv_last_cta(a.ctrl);
   __syncthreads();
   if (!s_last) return;
   if (kPaged)
-    for (int b = threadIdx.x; b < a.B; b += kJoinThreads) {
-      const int bits = a.bad[b];
-      if (bits) {
-        atomicOr(a.ctrl + sv::kKvCollect, bits);
-        a.bad[b] = 0;
-      }
-    }
+    for (int b = threadIdx.x; b < a.B; b += kJoinThreads) a.bad[b] = 0;
   __syncthreads();
   if (threadIdx.x == 0) sv::kv_publish(a.ctrl);
 }
