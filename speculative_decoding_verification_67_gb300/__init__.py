@@ -622,13 +622,13 @@ def spec_tree_verify_from_logits(target_logits, draft_logits, tokens, parents, u
 # ------------------------------------------------- cache operators: common
 def _one_device(first, name, *others):
     """The device of ``first``; every other given tensor must lie on it."""
-    if not first.is_cuda:
+    index = first.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = first.device
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must lie on {dev}, got one on {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must lie on {first.device}, got one on {t.device}")
+    return first.device
 
 
 class _Launch:

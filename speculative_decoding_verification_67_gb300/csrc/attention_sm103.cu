@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kLoadWarp) {
     // ------------------------------------------------------------- loads
     uint32_t loads = 0, segs = 0;
-    const uint64_t keep = sv::l2_policy_evict_last(), once = sv::l2_policy_evict_first();
+    const uint64_t keep = sv::l2_policy_evict_normal(), once = sv::l2_policy_evict_first();
     const int lw = warp - kLoadWarp;
     const bool issuer = elect_one();
     const uint64_t policy = a.S * a.G <= kBlock ? once : keep;  // whether another row tile reads the entries again
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int chunk = lane % kChunks, sub = lane / kChunks;
           int r0[kEach], r1[kEach] = {};  // rows of the block before, of this block; -1: zeros
           // whole blocks of the pool come in boxes of a.box rows of one page, the others row by row
-          auto boxed = [&](int j) { return a.box != 0 && j < committed && (j + 1) * kBlock <= limit; };
+          auto boxed = [&](int j) { return a.box != 0 && j < committed && limit - j * kBlock >= kBlock; };
           auto row_at = [&](int p) {  // the pool's row of a position
             const int col = p / a.page_size, page = table[col];
             if (page >= 0 && page < a.num_pages) return page * a.page_size + (p - col * a.page_size);
@@ -687,12 +687,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t to = sv::smem_u32(ring + slot * Sh::kTileBytes) + (chunk >> 3) * (kBlock * 128);
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-#pragma unroll 2
-              for (int i = (lw + e) % kCopyWarps; i < 32 / kAtOnce; i += kCopyWarps) {
+#pragma unroll
+              for (int k = 0; k < (32 / kAtOnce + kCopyWarps - 1) / kCopyWarps; ++k) {
+                const int i = k * kCopyWarps + lw;
                 const int in = i * kAtOnce + sub, spot = 32 * e + in;
-                const int row = __shfl_sync(0xffffffffu, r[e], in);
-                copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + (row < 0 ? 0 : row * entry),
-                        row < 0 ? 0 : 16);
+                const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
+                if (i < 32 / kAtOnce)
+                  copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + static_cast<unsigned>(max(row, 0)) * static_cast<unsigned long long>(static_cast<unsigned>(entry)),
+                          row < 0 ? 0 : 16);
               }
             }
             copies_arrive(&sh.full[slot]);

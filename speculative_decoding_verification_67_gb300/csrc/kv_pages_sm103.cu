@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_release_kernel(const PagesArgs
     int* row = row_of(a, b);
     const int c0 = to / a.page_size + (to % a.page_size != 0);
     int bad = 0;
-    for (int c = c0 + lane; c < a.max_pages; c += 32) {
+    for (long long c = c0 + lane; c < a.max_pages; c += 32) {
       const int p = row[c];
       if (p >= a.num_pages) bad |= SPEC_KV_DEVERR_PAGE;
       else if (p >= 0 && a.ref[p] < 1) bad |= SPEC_KV_DEVERR_REF;
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_release_kernel(const PagesArgs
       bits |= bad;
       continue;
     }
-    for (int c = c0 + lane; c < a.max_pages; c += 32) {
+    for (long long c = c0 + lane; c < a.max_pages; c += 32) {
       const int p = row[c];
       if (p < 0) continue;
       if (atomicSub(a.ref + p, 1) < 1) {  // more holders than the count says: put it back
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kRowThreads)
   if (!bad) {
     const int* from = row_of(a, s);
     const int* to = row_of(a, d);
-    for (int c = threadIdx.x; c < a.max_pages; c += kRowThreads) {
+    for (long long c = threadIdx.x; c < a.max_pages; c += kRowThreads) {
       if (to[c] >= 0) bad |= SPEC_KV_DEVERR_BUSY;
       if (c >= used) continue;
       const int p = from[c];
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kRowThreads)
   if (s_bad == 0) {
     const int* from = row_of(a, s);
     int* to = row_of(a, d);
-    for (int c = threadIdx.x; c < a.max_pages; c += kRowThreads) {
+    for (long long c = threadIdx.x; c < a.max_pages; c += kRowThreads) {
       int p = -1;
       if (c < used) {
         p = from[c];
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(const PagesArg
   if (threadIdx.x == 0) s_err = 0;
   __syncthreads();
   long long mine = 0, sum;
-  for (int p = threadIdx.x; p < a.num_pages; p += kPlanThreads) {
+  for (long long p = threadIdx.x; p < a.num_pages; p += kPlanThreads) {
     const int r = a.ref[p];
     mine += r > 0;
     if (r < 0) atomicOr(&s_err, SPEC_KV_DEVERR_REF);
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(const PagesArg
   const int holes = collect_pages(a.ref, 0, live, false, live, a.list, warp_sum);
   collect_pages(a.ref, live, a.num_pages, true, holes, a.olds, warp_sum);
   // where each page at or behind `live` goes (cnt serves as the map); -1 for a free one
-  for (int p = live + threadIdx.x; p < a.num_pages; p += kPlanThreads) a.cnt[p] = -1;
+  for (long long p = static_cast<long long>(live) + threadIdx.x; p < a.num_pages; p += kPlanThreads) a.cnt[p] = -1;
   __syncthreads();
   for (int k = threadIdx.x; k < holes; k += kPlanThreads) {
     const int to = a.list[k], from = a.olds[k];

@@ -506,3 +506,97 @@ def test_a_speculative_round_on_the_cache():
         want = attention.rows(np64(nq[b]), np64(keys[:, 0]), np64(keys[:, 1]), np.ones((1, len(keys)), bool),
                               D ** -0.5)
         check(got[b], None, want, D, torch.bfloat16, len(keys), float(pool.abs().max()))
+
+
+# --------------------------------------------------------------- the far ends
+def test_nothing_to_do():
+    c = Cache([40, 9], 3, 4, 2, 64, torch.bfloat16, 16, True, seed=2)
+    out, lse, err = c.run(q_len=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert err == 0 and (out == 7).all() and (lse == 7).all()
+    q, k, v, _, _ = prompts([5], [0], 4, 2, 64, torch.float16)
+    out = torch.full_like(q, 7.0)
+    sv.spec_prompt_attention(q, k, v, torch.zeros(4, dtype=torch.int32, device="cuda"), out=out)
+    assert (out == 7).all()
+
+
+def test_pool_beyond_32_bits_of_bytes_and_elements():
+    """Pages at the far end of a pool of 9.7 GB; pages named by two sequences, and twice by one."""
+    kv_heads, D, page, entry = 8, 128, 16, 2048
+    pages = 148000
+    pool = torch.empty((pages, page, entry), dtype=torch.bfloat16, device="cuda")
+    used = list(range(pages - 12, pages)) + [0, 1]
+    pool[used] = torch.randn((len(used), page, entry), device="cuda").bfloat16()
+    c = Cache([150, 150, 100], 2, 8, kv_heads, D, torch.bfloat16, page, False, seed=1)
+    c.pool = pool
+    table = torch.full((3, 11), -1, dtype=torch.int32)
+    table[0, :10] = torch.tensor(used[:10])
+    table[1, :10] = torch.tensor(used[:9] + [used[10]])
+    table[2, :7] = torch.tensor([used[12], used[13], used[12], used[3], used[4], used[5], used[11]])
+    c.table = table.cuda()
+    out, lse, err = c.run()
+    assert err == 0
+    for b in range(3):
+        check(out[b], lse[b], c.want(b), D, c.dtype, 152, 6.0)
+
+
+def test_most_heads_and_single_token_strides():
+    c = Cache([20, 150], 1, 1024, 1024, 64, torch.bfloat16, 16, True, seed=3)
+    out, lse, err = c.run()
+    assert err == 0
+    for b in range(2):
+        check(out[b], lse[b], c.want(b), 64, c.dtype, c.lens[b] + 1, c.vmax())
+    c = Cache([20, 150, 3], 1, 4, 2, 128, torch.float16, 16, False, seed=4)
+    wide = torch.randn((3, 1, 12, 128), device="cuda").half()
+    c.q = wide[:, :, 4:8]
+    out, lse, err = c.run()
+    assert err == 0
+    for b in range(3):
+        check(out[b], lse[b], c.want(b), 128, c.dtype, c.lens[b] + 1, c.vmax())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, over and over."""
+    a = Cache([700, 30], 1, 8, 2, 128, torch.bfloat16, 16, False, seed=5)
+    q, k, v, cq, _ = prompts([300, 200], [0, 0], 8, 2, 128, torch.bfloat16, seed=6)
+    want_a, _, _ = a.run()
+    want_p = sv.spec_prompt_attention(q, k, v, cq)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    wa, wp = sv.kv_attention_workspace(a.q, a.pool), sv.prompt_attention_workspace(q, k, 2)
+    torch.cuda.synchronize()
+    got_a, got_p = [], []
+    for _ in range(10):
+        got_a.append(sv.spec_kv_attention(a.q, a.pool, a.table, a.seq_len, workspace=wa, stream=s1))
+        got_p.append(sv.spec_prompt_attention(q, k, v, cq, workspace=wp, stream=s2))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want_a) for x in got_a) and all(torch.equal(x, want_p) for x in got_p)
+
+
+def test_spoiled_first_blocks_and_many_spoiled_rows():
+    """NaN and infinite values in the only block of an item, and in all of a block's later tokens."""
+    q, k, v, cq, ck = prompts([100, 260], [0, 0], 2, 1, 128, torch.bfloat16, seed=8)
+    v[20] = float("inf")
+    v[100 + 130:] = float("nan")
+    out = sv.spec_prompt_attention(q, k, v, cq)
+    check_prompts(q[:20], k[:20], v[:20], cq[:2].clamp(max=20), cq[:2].clamp(max=20), out[:20], None, torch.bfloat16)
+    assert (out[20:100] == float("inf")).all()
+    assert torch.isfinite(out[100:230]).all() and out[230:].isnan().all()
+    c = torch.tensor([0, 130], dtype=torch.int32, device="cuda")
+    check_prompts(q[100:230], k[100:230], v[100:230], c, c, out[100:230], None, torch.bfloat16)
+
+
+@pytest.mark.parametrize("staged", [False, True])
+def test_rising_scores(staged):
+    """Every block's scores far above the last one's, and far below: the reference moves, or stays."""
+    for sign in (1.0, -1.0):
+        c = Cache([1000], 2, 2, 1, 64, torch.bfloat16, 16, staged, seed=9)
+        c.q[:] = 1.0
+        ramp = torch.arange(1000, device="cuda") // 100 * sign * 0.5
+        for p in range(1000):
+            c.pool[int(c.table[0, p // 16]), p % 16, :64] += ramp[p].to(torch.bfloat16)
+        c.check()
+    for dtype in (torch.bfloat16, torch.float16):
+        q, k, v, cq, ck = prompts([600], [0], 2, 2, 64, dtype, seed=10)
+        q[:] = 1.0
+        k += (torch.arange(600, device="cuda") // 60).to(dtype)[:, None, None]
+        out = sv.spec_prompt_attention(q, k, v, cq)
+        check_prompts(q, k, v, cq, ck, out, None, dtype, rows=np.arange(0, 600, 7))
