@@ -287,6 +287,14 @@ struct Shape {
   static constexpr int kTileBytes = kBlock * D * 2;
   static constexpr int kStages = D == 64 ? 8 : (kPaged ? 5 : 4);
   static constexpr int kQBytes = kTiles<kPaged> * kTileBytes;
+  // Where 64 columns (128 bytes) of a row of a K or V tile lie: rows in groups of eight (the unit of the swizzle and
+  // of the matrix descriptors).  Prompts: all rows of the first 64 columns, then of the others, as a box of token rows
+  // brings them.  Cache: both halves of a group together, so that one box brings whole rows of a page.
+  static constexpr int kGroup = kPaged ? D / 64 * 1024 : 1024;
+  static constexpr int kHalf = kPaged ? 1024 : kBlock * 128;
+  static __device__ __forceinline__ uint32_t spot(int row, int piece) {  // byte of a row's 16-byte piece
+    return (row >> 3) * kGroup + (piece >> 3) * kHalf + (row & 7) * 128 + (((piece & 7) ^ (row & 7)) << 4);
+  }
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 256;  // O accumulators behind the two score tiles
 };
@@ -673,18 +681,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               for (int i = lw; i < boxes; i += kCopyWarps) {
                 const int row = __shfl_sync(0xffffffffu, r[0], i);
-                if (issuer) {
-#pragma unroll
-                  for (int h = 0; h < D / 64; ++h)
-                    sv::tma_load_2d(dst + h * (kBlock * 128) + i * a.box * 128, &map_k, &sh.full[slot],
-                                    head * D + h * 64, row, policy);
-                }
+                if (issuer)
+                  sv::tma_load_4d(dst + i * a.box / 8 * Sh::kGroup, &map_k, &sh.full[slot], 0, 0, head * (D / 64), row / 8,
+                                  policy);
                 __syncwarp();
               }
               return;
             }
             const char* from = static_cast<const char*>(j >= committed ? a.staged : a.k) + head * (D * 2) + chunk * 16;
-            const uint32_t to = sv::smem_u32(ring + slot * Sh::kTileBytes) + (chunk >> 3) * (kBlock * 128);
+            const uint32_t to = sv::smem_u32(ring + slot * Sh::kTileBytes);
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
 #pragma unroll
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int in = i * kAtOnce + sub, spot = 32 * e + in;
                 const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
                 if (i < 32 / kAtOnce)
-                  copy_16(to + spot * 128 + (((chunk & 7) ^ (spot & 7)) << 4), from + static_cast<unsigned>(max(row, 0)) * static_cast<unsigned long long>(static_cast<unsigned>(entry)),
+                  copy_16(to + Sh::spot(spot, chunk), from + static_cast<unsigned>(max(row, 0)) * static_cast<unsigned long long>(static_cast<unsigned>(entry)),
                           row < 0 ? 0 : 16);
               }
             }
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!aborted(sh)) {
                 sv::mbar_arrive_expect_tx(&sh.full[slot], Sh::kTileBytes);
                 for (int h = 0; h < D / 64; ++h)
-                  sv::tma_load_3d(ring + slot * Sh::kTileBytes + h * (kBlock * 128), kv ? &map_v : &map_k,
+                  sv::tma_load_3d(ring + slot * Sh::kTileBytes + h * Sh::kHalf, kv ? &map_v : &map_k,
                                   &sh.full[slot], h * 64, at.kvh, static_cast<int>(at.s.k0) + j * kBlock, keep);
               }
               ++loads;
@@ -764,12 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scores = [&](int t, uint32_t k_addr) {
         const uint32_t qa = __shfl_sync(0xffffffffu, q_addr + (kPaged ? 0 : t * Sh::kTileBytes), 0);
         const uint32_t ka = __shfl_sync(0xffffffffu, k_addr, 0), d = __shfl_sync(0xffffffffu, tmem + t * kBlock, 0);
-        const uint64_t q_desc = sv::smem_desc_k_sw128(qa), k_desc = sv::smem_desc_k_sw128(ka);
+        const uint64_t q_desc = sv::smem_desc_k_sw128(qa), k_desc = sv::smem_desc_k_sw128(ka, Sh::kGroup);
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k / 4) * (kBlock * 128) + (k % 4) * 32) >> 4;
-            sv::mma_bf16_ss(d, q_desc + off, k_desc + off, kIdS, k > 0);
+            const uint32_t in = (k % 4) * 32;
+            sv::mma_bf16_ss(d, q_desc + (((k / 4) * (kBlock * 128) + in) >> 4), k_desc + (((k / 4) * Sh::kHalf + in) >> 4),
+                            kIdS, k > 0);
           }
           sv::mma_commit(&sh.s_full[t]);
         }
@@ -783,12 +789,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         sv::tc_fence_after_sync();
         const uint32_t fresh = first && !*reinterpret_cast<volatile int*>(&sh.o_set[t]);
         const uint32_t va = __shfl_sync(0xffffffffu, v_addr, 0), p = __shfl_sync(0xffffffffu, tmem + t * kBlock, 0);
-        const uint64_t v_desc = sv::smem_desc_mn_sw128(va, kBlock * 128);
+        const uint64_t v_desc = sv::smem_desc_mn_sw128(va, Sh::kHalf, Sh::kGroup);
         const uint32_t go = __shfl_sync(0xffffffffu, fresh ^ 1u, 0), d = p - t * kBlock + Sh::kO + t * D;
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k)
-            sv::mma_f16_ts(d, p + k * 8, v_desc + k * (2048 >> 4), kIdO, k > 0 ? 1u : go);
+            sv::mma_f16_ts(d, p + k * 8, v_desc + k * (2 * Sh::kGroup >> 4), kIdO, k > 0 ? 1u : go);
         }
         __syncwarp();
       };
@@ -951,12 +957,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int bar = pair ? 3 : 1 + t, crowd = pair ? 256 : 128;
           const uint32_t rank = loads + v_rank<kPaged>(i, nb), slot = rank % Sh::kStages;
           wait(&sh.full[slot], rank / Sh::kStages & 1);
-          uint8_t* vrow = ring + slot * Sh::kTileBytes + row * 128;
+          uint8_t* tile = ring + slot * Sh::kTileBytes;
           const int chunks = D / 8 / parts, c0 = part * chunks;
           bool odd = false;
           for (int c = c0; c < c0 + chunks; ++c) {
-            const uint4 w =
-                *reinterpret_cast<const uint4*>(vrow + (c >> 3) * (kBlock * 128) + (((c & 7) ^ (row & 7)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + Sh::spot(row, c));
             odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
           }
           const unsigned word = __ballot_sync(0xffffffffu, odd);
@@ -969,8 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               (warp & 2) ? ((warp & 1) ? spoil[3] : spoil[2]) : ((warp & 1) ? spoil[1] : spoil[0]);
           if (own >> lane & 1u) {
             for (int c = c0; c < c0 + chunks; ++c)
-              *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kBlock * 128) + (((c & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + Sh::spot(row, c)) = make_uint4(0, 0, 0, 0);
             sv::fence_proxy_async_smem();
           }
           meet(bar, crowd);
@@ -1423,13 +1427,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A 16-bit tensor with boxes of 64 elements (128 bytes, 128-byte swizzle) by box_y by box_z, zeros outside.
-bool encode(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t (&dim)[3], const uint64_t (&stride)[2],
-            uint32_t box_y, uint32_t box_z) {
+// A 16-bit tensor with boxes of 64 elements (128 bytes, 128-byte swizzle) by box[1], .., zeros outside; strides in
+// bytes, from the second dimension on.
+bool encode(CUtensorMap* map, int dtype, const void* base, int rank, const cuuint64_t (&dims)[4],
+            const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
   const auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {dim[0], dim[1], dim[2]}, strides[2] = {stride[0], stride[1]};
-  const cuuint32_t box[3] = {64, box_y, box_z}, step[3] = {1, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
   return fn(map, dtype == SPEC_ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1438,9 +1442,11 @@ bool encode(CUtensorMap* map, int dtype, const void* base, int rank, const uint6
 
 bool encode_tokens(CUtensorMap* map, int dtype, const void* base, int head_dim, int heads, int64_t tokens,
                    int64_t stride, int box_heads, int box_tokens) {
-  return encode(map, dtype, base, 3,
-                {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)},
-                {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(stride) * 2}, box_heads, box_tokens);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens), 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(stride) * 2, 0};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens), 1};
+  return encode(map, dtype, base, 3, dims, strides, box);
 }
 
 template <typename T, int D, bool kPaged>
@@ -1546,15 +1552,18 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   // Boxes of at least eight rows; below that one copy of 16 bytes per thread is faster.
   // Up to 16 rows (one token) a piece is next to nothing to join.
   a.least = dims.S * a.G <= 16 ? 1 : 4;
-  a.join_split = dims.S * a.G <= 16 ? 1 : 4;
+  a.join_split = dims.S * a.G <= 8 ? 1 : (dims.S * a.G < 64 ? (dims.S * a.G + 7) / 8 : 8);
   a.box = kBlock;
   while (a.box >= 8 && dims.page_size % a.box != 0) a.box /= 2;
   if (a.box < 8) a.box = 0;
-  const int64_t entry = 2ll * dims.kv_heads * dims.head_dim;
-  if (!encode(&maps[1], dims.dtype, pool, 2,
-              {static_cast<uint64_t>(entry), static_cast<uint64_t>(dims.num_pages) * dims.page_size, 1},
-              {static_cast<uint64_t>(entry) * 2, 0}, a.box ? a.box : 1, 1))
-    return SPEC_ERR_CUDA;
+  maps[1] = maps[0];
+  if (a.box) {  // (64 columns, eight rows, the columns' places in the entry, groups of eight rows)
+    const cuuint64_t entry = 2ull * dims.kv_heads * dims.head_dim;
+    const cuuint64_t dim[4] = {64, 8, entry / 64, static_cast<cuuint64_t>(dims.num_pages) * dims.page_size / 8};
+    const cuuint64_t stride[3] = {entry * 2, 128, entry * 16};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(dims.head_dim / 64), static_cast<cuuint32_t>(a.box / 8)};
+    if (!encode(&maps[1], dims.dtype, pool, 4, dim, stride, box)) return SPEC_ERR_CUDA;
+  }
   maps[2] = maps[1];  // (not used)
   return launch<true>(a, maps, dims.head_dim, dims.dtype, dev, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

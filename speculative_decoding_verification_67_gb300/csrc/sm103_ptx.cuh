@@ -210,6 +210,16 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// 4-D tiled load.
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Allocation of `ncols` (power of two, >= 32) TMEM columns by one whole warp;
 // the base address is written to shared memory.
@@ -261,12 +271,12 @@ __device__ __forceinline__ void tc_fence_after_sync() {
 // byte offset unused for this layout (encoded 1), fixed field 0b001 at bit 46,
 // swizzle mode 2 (128 B) at bits 61-63.  The tile must start on 1024 bytes;
 // a K step inside the 128-byte row is taken by adding its byte offset to
-// the start address.
-__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
+// the start address.  (Groups may lie `group_bytes` apart instead.)
+__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr, uint32_t group_bytes = 1024) {
   uint64_t desc = 0;
   desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
   desc |= static_cast<uint64_t>(1) << 16;
-  desc |= static_cast<uint64_t>(1024 >> 4) << 32;
+  desc |= static_cast<uint64_t>(group_bytes >> 4) << 32;
   desc |= static_cast<uint64_t>(1) << 46;
   desc |= static_cast<uint64_t>(2) << 61;
   return desc;
@@ -434,13 +444,12 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 
 // Shared-memory matrix descriptor of an MN-major operand: rows of 128 bytes
 // (64 elements of the M or N dimension), one per K index, 128-byte swizzle.
-// Eight K rows make a group of 1024 bytes (stride byte offset between groups);
-// the next 64 elements of M or N lie `lbo` bytes on (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+// Eight K rows make a group of 1024 bytes, groups lie `group_bytes` apart; the next 64 elements of M or N lie `lbo` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t group_bytes) {
   uint64_t desc = 0;
   desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
   desc |= static_cast<uint64_t>(lbo >> 4) << 16;
-  desc |= static_cast<uint64_t>(1024 >> 4) << 32;
+  desc |= static_cast<uint64_t>(group_bytes >> 4) << 32;
   desc |= static_cast<uint64_t>(1) << 46;
   desc |= static_cast<uint64_t>(2) << 61;
   return desc;
