@@ -1551,7 +1551,7 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
     return SPEC_ERR_CUDA;
   // Boxes of at least eight rows; below that one copy of 16 bytes per thread is faster.
   // Up to 16 rows (one token) a piece is next to nothing to join.
-  a.least = dims.S * a.G <= 16 ? 1 : 4;
+  a.least = dims.S * a.G <= 16 ? 1 : 3;
   a.join_split = dims.S * a.G <= 8 ? 1 : (dims.S * a.G < 64 ? (dims.S * a.G + 7) / 8 : 8);
   a.box = kBlock;
   while (a.box >= 8 && dims.page_size % a.box != 0) a.box /= 2;
@@ -1600,7 +1600,7 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
   a.v_stride = dims.v_stride;
   a.tile_tokens = kBlock / a.G;
   a.least = 6;
-  a.join_split = 4;
+  a.join_split = 8;
   CUtensorMap maps[3];
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, dims.total_q, dims.q_stride, a.G,
                      a.tile_tokens) ||
