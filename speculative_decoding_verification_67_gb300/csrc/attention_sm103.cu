@@ -215,6 +215,23 @@ __device__ __noinline__ long long floor_sum(long long n, long long m, long long 
   return sum;
 }
 
+// sum over i < n of floor((span i + y) / kBlock).  For spans that divide a block
+// (groups of 2, 4, 8, ..) the terms repeat, for their multiples they rise evenly;
+// the general recursion costs about ten divisions.
+__device__ __forceinline__ long long step_sum(long long n, int span, int y) {
+  if (kBlock % span == 0) {
+    const int m = kBlock / span, shift = __ffs(m) - 1;
+    auto upto = [&](long long t) {  // sum over i < t of floor(i / m)
+      const long long q = t >> shift;
+      return m * (q * (q - 1) / 2) + (t - (q << shift)) * q;
+    };
+    const long long from = y / span;
+    return upto(from + n) - upto(from);
+  }
+  if (span % kBlock == 0) return n * (y / kBlock) + n * (n - 1) / 2 * (span / kBlock);
+  return floor_sum(n, kBlock, span, y);
+}
+
 // Units (blocks and kItemUnits each) of the first t items of one head of a sequence.
 template <bool kPaged>
 __device__ __noinline__ long long head_units(const AttnArgs& a, const Seq s, int t) {
@@ -222,9 +239,10 @@ __device__ __noinline__ long long head_units(const AttnArgs& a, const Seq s, int
   if (kPaged) return sum + static_cast<long long>(t) * item_blocks<kPaged>(a, s, 0);
   const int span = a.tile_tokens * 2;
   const int full = t < s.tiles ? t : s.tiles - 1;  // tiles whose last token is (i + 1) span - 1
-  int none = s.base < 0 ? -s.base / span : 0;      // tiles that see nothing: one block each
-  if (none > full) none = full;
-  sum += none + floor_sum(full - none, kBlock, span, s.base + static_cast<long long>(none + 1) * span + kBlock - 1);
+  int none = 0;                                    // tiles that see nothing: one block each
+  if (s.base < 0) none = min(full, -s.base / span);
+  // + sum over the others of ceil((base + (i + 1) span) / kBlock)
+  sum += none + step_sum(full - none, span, s.base + (none + 1) * span + kBlock - 1);
   if (t == s.tiles) sum += item_blocks<kPaged>(a, s, t - 1);
   return sum;
 }
@@ -379,13 +397,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-// Whether a packed pair holds an infinity or a NaN (all exponent bits set).
-__device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Adds 0 to `sum` for two finite values, NaN for an infinity or a NaN.
+__device__ __forceinline__ __nv_bfloat162 taint(uint32_t w, __nv_bfloat162 sum) {
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.f), sum);
 }
-__device__ __forceinline__ bool odd_pair(uint32_t w, __half) {
-  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+__device__ __forceinline__ __half2 taint(uint32_t w, __half2 sum) {
+  return __hfma2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(0.f), sum);
 }
+__device__ __forceinline__ bool tainted(__nv_bfloat162 s) { return __hisnan(s.x) || __hisnan(s.y); }
+__device__ __forceinline__ bool tainted(__half2 s) { return __hisnan(s.x) || __hisnan(s.y); }
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ type zero() { return __float2bfloat162_rn(0.f); }
+};
+template <>
+struct Pair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ type zero() { return __float2half2_rn(0.f); }
+};
 
 // Two products and sums in one instruction.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
@@ -959,11 +991,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&sh.full[slot], rank / Sh::kStages & 1);
           uint8_t* tile = ring + slot * Sh::kTileBytes;
           const int chunks = D / 8 / parts, c0 = part * chunks;
-          bool odd = false;
+          typename Pair<T>::type sum0 = Pair<T>::zero(), sum1 = sum0;
+#pragma unroll 1
           for (int c = c0; c < c0 + chunks; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(tile + Sh::spot(row, c));
-            odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
+            sum0 = taint(w.x, taint(w.y, sum0));
+            sum1 = taint(w.z, taint(w.w, sum1));
           }
+          const bool odd = tainted(sum0) || tainted(sum1);
           const unsigned word = __ballot_sync(0xffffffffu, odd);
           if (lane == 0) sh.spoiled[box][part][warp & 3] = word;
           meet(bar, crowd);
