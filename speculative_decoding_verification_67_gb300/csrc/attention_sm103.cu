@@ -4,41 +4,56 @@
 // One kernel for both.  A work item is a tile of query rows of one key-value
 // head: row r of a tile is token r / G, head r % G of the group (G = heads /
 // kv_heads), so a key or value is fetched once for all heads that share it.
-// The item walks its keys in blocks of 128 with the running maximum and sum of
-// the softmax:
+// The item walks its keys in blocks of 128 with the running reference m and sum
+// of the softmax:
 //   S = Q K^T            tcgen05.mma, 128 x 128, operands in shared memory
 //   P = exp2(S c - m c)  softmax warps, S read from and P written to TMEM
 //   O = O + P V          tcgen05.mma, P from TMEM, V from shared memory
-// with c = scale log2(e).  m is raised, and O rescaled, only when a row's new
-// maximum exceeds it by more than 2^8 in weight; until then weights up to 2^8
-// stand in P, which costs no precision and spares reading O back for most
-// blocks.
+// with c = scale log2(e).  m is a maximum of the row; it is raised, and O
+// rescaled, only when a later maximum exceeds it by more than 2^8 in weight.
+// Until then weights up to 2^8 stand in P, which costs no precision and spares
+// reading O back for most blocks.  P is rounded to the input type, because that
+// is what the tensor core multiplies; the sum is of the unrounded weights.
 //
 // Two softmax warpgroups (one row per thread) work on two score tiles, so the
 // tensor core computes for one while the other is in its exponentials:
 //   * prompts: two row tiles of the item share every K and V block;
 //   * cache: the item has one row tile, the warpgroups take even and odd
-//     blocks, each with a running maximum, sum and O of its own, merged at the
-//     end.  With few rows (one token: G of the 128 rows) the tensor core's
-//     work is padding, but at 1024 clocks a block it stays below the ~2200 that
-//     a block's 64 KB take from HBM, which is what bounds it.
+//     blocks, each with a reference, sum and O of its own, merged at the end.
+//     With few rows (one token: G of the 128 rows) the tensor core's work is
+//     padding, but at 1024 clocks a block it stays below the ~2200 that a
+//     block's 64 KB take from HBM.
+// Tensor memory is full: two score tiles (P over the scores it came from) and
+// two O.  So a tile's next scores wait for its last P V, and a tile's block takes
+// the products' 1024 clocks and ~500 of their latency after the ~1900 of its
+// softmax; two tiles overlap to ~3200 clocks per two blocks.  That chain
+// bounds long prompts (73 % of the measured bf16 rate), HBM the cache form
+// with a full batch, and start, end and join of the items everything short.
 //
 // One CTA per SM walks an equal share of all items' blocks (plus a constant per
 // item for its start and end).  An item cut between CTAs leaves unnormalised
-// partial rows, which a second, small kernel joins.  Shares are computed from the lengths
-// on the device; the host never sees them.
+// partial rows, which a second, small kernel joins in the order of the pieces.
+// Shares are computed from the lengths on the device; the host never sees them.
+// Both kernels may start while what came before them on the stream ends, and
+// wait for it before they touch memory.
 //
-// Loads: a warp feeds a ring of 128-position K and V tiles by TMA.  Packed
-// keys are boxes of 128 token rows.  Cache positions are looked up in the block table and
-// fetched by four-row gathers, so pages of any size, in any place, and staged
-// entries make the same tile; positions behind the end are rows outside the
-// tensor and arrive as zeros.
+// Loads: a ring of 128-position K and V tiles.  Packed keys are TMA boxes of 128
+// token rows.  Over the cache whole blocks come as boxes of up to 128 rows of
+// one page (every size divisible by 8), partial blocks, staged entries and
+// other pages row by row with cp.async; rows behind the end are zeros.  Boxes
+// of 16 rows and more stream B = 64 caches at 6.0 TB/s, boxes of eight at 5.2,
+// rows at 3.9.
 //
 // Masked values: P is 0 where a row must not see a key, but 0 times an
 // infinite or not-a-number value is not 0.  In blocks that some row may not
 // see to the end, the softmax warps look through the V tile first: rows of V
 // with such values are zeroed in shared memory and added, to the rows that do
 // see them, by plain multiplications.
+//
+// Measured (GB300, calls one after the other): one prompt of 12301 tokens, 32
+// heads over 8, 0.89 ms (1.40 PFLOP/s); 16 prompts of up to 2047 tokens 237 us
+// (0.77); 64 caches of up to 8191 positions, one token each, 193 us; one cache
+// of 1000 positions 12 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int committed = a.staged ? blocks_of(at.s.base) : at.n;  // blocks read from the pool
           const int limit = a.staged ? at.s.base : at.s.base + at.s.Lq;
           const int* table = a.bt + static_cast<long long>(at.b) * a.max_pages;
-          const long long entry = 4ll * a.kv_heads * D;  // bytes
+          const unsigned long long entry = 4ull * a.kv_heads * D;  // bytes
           constexpr int kEach = kBlock / 32;             // rows a lane looks up: lane, lane + 32, ..
           constexpr int kChunks = D / 8;                 // 16-byte pieces of a row
           constexpr int kAtOnce = 32 / kChunks;          // rows one instruction copies
@@ -730,8 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int in = i * kAtOnce + sub, spot = 32 * e + in;
                 const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
                 if (i < 32 / kAtOnce)
-                  copy_16(to + Sh::spot(spot, chunk), from + static_cast<unsigned>(max(row, 0)) * static_cast<unsigned long long>(static_cast<unsigned>(entry)),
-                          row < 0 ? 0 : 16);
+                  copy_16(to + Sh::spot(spot, chunk), from + static_cast<unsigned>(max(row, 0)) * entry, row < 0 ? 0 : 16);
               }
             }
             copies_arrive(&sh.full[slot]);
@@ -851,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i + 2 >= nb) commit(&sh.o_full[t]);
             if (i + 2 < nb) {
               const uint32_t k_addr = arrived();
-                scores(t, k_addr);
+              scores(t, k_addr);
               commit(&sh.empty[loads++ % Sh::kStages]);
               if (i + 3 == nb) commit(&sh.q_empty);
             }
@@ -873,11 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i + 1 < nb) {
               k_addr = arrived();
               k_slot = loads++ % Sh::kStages;
-                scores(0, k_addr);
+              scores(0, k_addr);
             }
-            if (two) {
-              values(1, v_addr, i == 0);
-              }
+            if (two) values(1, v_addr, i == 0);
             commit(&sh.empty[v_slot]);
             if (two && i + 1 == nb) commit(&sh.o_full[1]);
             if (i + 1 < nb) {
@@ -1584,10 +1596,11 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
   CUtensorMap maps[3];
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, tokens, dims.q_stride, a.G, a.tile_tokens))
     return SPEC_ERR_CUDA;
-  // Boxes of at least eight rows; below that one copy of 16 bytes per thread is faster.
-  // Up to 16 rows (one token) a piece is next to nothing to join.
+  // Up to 16 rows (one token) a piece is next to nothing to join: with 1, 2 and 3 units one cache of 1000 positions took
+  // 12.2, 13.6 and 14.7 us; a tree of 120 rows over 4 caches 19.0, 20.2 and 24.0 with 3, 4 and 6.
   a.least = dims.S * a.G <= 16 ? 1 : 3;
   a.join_split = dims.S * a.G <= 8 ? 1 : (dims.S * a.G < 64 ? (dims.S * a.G + 7) / 8 : 8);
+  // the largest boxes that pages and blocks divide into; below eight rows (the swizzle's unit) row by row
   a.box = kBlock;
   while (a.box >= 8 && dims.page_size % a.box != 0) a.box /= 2;
   if (a.box < 8) a.box = 0;
@@ -1634,7 +1647,7 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
   a.k_stride = dims.k_stride;
   a.v_stride = dims.v_stride;
   a.tile_tokens = kBlock / a.G;
-  a.least = 6;
+  a.least = 6;  // (four heads over three short prompts: 18.4 us; 20.1 with 4, 23.2 with 8)
   a.join_split = 8;
   CUtensorMap maps[3];
   if (!encode_tokens(&maps[0], dims.dtype, q, dims.head_dim, dims.heads, dims.total_q, dims.q_stride, a.G,
