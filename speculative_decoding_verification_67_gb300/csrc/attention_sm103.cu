@@ -1318,7 +1318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // traffic, bound by two dependent loads (the record, then all the rest).
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  constexpr int kNT = kTiles<kPaged>, kE = D / 32, kWarps = kJoinThreads / 32;
+  constexpr int kNT = kTiles<kPaged>, kE = D / 32, kWarps = kJoinThreads / 32, kFew = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sv::griddep_wait();
   sv::griddep_launch_dependents();
@@ -1337,45 +1337,73 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     float o[kE], ref = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] = 0.f;
-    for (int p0 = cut.first; p0 <= last; p0 += 32) {  // (one round for up to 32 pieces)
-      const float2 ml = p0 + lane <= last ? a.part_ml[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
-      constexpr int kAhead = 8;
-      float x[kAhead][kE];
-      auto fetch = [&](int q0) {
+    if (last - cut.first < kFew) {  // a few pieces (most items): all at once
+      float2 ml[kFew];
+      float x[kFew][kE];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          if (q0 + q > last) continue;
-          const float* from = a.part_o + place(q0 + q) * D + lane * kE;
+      for (int q = 0; q < kFew; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        if (cut.first + q > last) continue;
+        const long long at = place(cut.first + q);
+        ml[q] = a.part_ml[at];
 #pragma unroll
-          for (int e = 0; e < kE; e += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(from + e);
-            x[q][e] = v.x;
-            x[q][e + 1] = v.y;
-          }
+        for (int e = 0; e < kE; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kE + e);
+          x[q][e] = v.x;
+          x[q][e + 1] = v.y;
         }
-      };
-      fetch(p0);
-      float top = ml.x;
+      }
 #pragma unroll
-      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      top = fmaxf(top, ref);
-      const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
-      const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
-      ref = top;
-      sum = keep == 0.f ? 0.f : sum * keep;
+      for (int q = 0; q < kFew; ++q) ref = fmaxf(ref, ml[q].x);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
-      const float l = f == 0.f ? 0.f : ml.y * f;
-      const int n = min(32, last - p0 + 1);
-      for (int p = 0; p < n; p += kAhead) {
-        if (p > 0) fetch(p0 + p);
+      for (int q = 0; q < kFew; ++q) {
+        if (ml[q].x == -INFINITY) continue;  // no such piece, or it saw no key
+        const float f = exp2_approx(ml[q].x - ref);
+        sum += ml[q].y * f;
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          const float w = __shfl_sync(0xffffffffu, f, (p + q) & 31);
-          sum += __shfl_sync(0xffffffffu, l, (p + q) & 31);  // (0 behind the last piece)
-          if (w != 0.f) {
+        for (int e = 0; e < kE; ++e) o[e] += x[q][e] * f;
+      }
+    } else {
+      for (int p0 = cut.first; p0 <= last; p0 += 32) {  // (one round for up to 32 pieces)
+        const float2 ml = p0 + lane <= last ? a.part_ml[place(p0 + lane)] : make_float2(-INFINITY, 0.f);
+        constexpr int kAhead = 8;
+        float x[kAhead][kE];
+        auto fetch = [&](int q0) {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) o[e] += x[q][e] * w;
+          for (int q = 0; q < kAhead; ++q) {
+            if (q0 + q > last) continue;
+            const float* from = a.part_o + place(q0 + q) * D + lane * kE;
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(from + e);
+              x[q][e] = v.x;
+              x[q][e + 1] = v.y;
+            }
+          }
+        };
+        fetch(p0);
+        float top = ml.x;
+#pragma unroll
+        for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        top = fmaxf(top, ref);
+        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
+        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
+        ref = top;
+        sum = keep == 0.f ? 0.f : sum * keep;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
+        const float l = f == 0.f ? 0.f : ml.y * f;
+        const int n = min(32, last - p0 + 1);
+        for (int p = 0; p < n; p += kAhead) {
+          if (p > 0) fetch(p0 + p);
+#pragma unroll
+          for (int q = 0; q < kAhead; ++q) {
+            const float w = __shfl_sync(0xffffffffu, f, (p + q) & 31);
+            sum += __shfl_sync(0xffffffffu, l, (p + q) & 31);  // (0 behind the last piece)
+            if (w != 0.f) {
+#pragma unroll
+              for (int e = 0; e < kE; ++e) o[e] += x[q][e] * w;
+            }
           }
         }
       }
