@@ -27,7 +27,7 @@
 // two O.  So a tile's next scores wait for its last P V, and a tile's block takes
 // the products' 1024 clocks and ~500 of their latency after the ~1900 of its
 // softmax; two tiles overlap to ~3200 clocks per two blocks.  That chain
-// bounds long prompts (73 % of the measured bf16 rate), HBM the cache form
+// bounds long prompts (70-73 % of the measured bf16 rate), HBM the cache form
 // with a full batch, and start, end and join of the items everything short.
 //
 // One CTA per SM walks an equal share of all items' blocks (plus a constant per
@@ -41,8 +41,8 @@
 // token rows.  Over the cache whole blocks come as boxes of up to 128 rows of
 // one page (every size divisible by 8), partial blocks, staged entries and
 // other pages row by row with cp.async; rows behind the end are zeros.  Boxes
-// of 16 rows and more stream B = 64 caches at 6.0 TB/s, boxes of eight at 5.2,
-// rows at 3.9.
+// of 16 rows and more stream B = 64 caches at 5.9 TB/s, boxes of eight at 5.5,
+// rows at 3.7 (pages of 100 positions) and 2.8 (pages of one).
 //
 // Masked values: P is 0 where a row must not see a key, but 0 times an
 // infinite or not-a-number value is not 0.  In blocks that some row may not
@@ -51,9 +51,10 @@
 // see them, by plain multiplications.
 //
 // Measured (GB300, calls one after the other): one prompt of 12301 tokens, 32
-// heads over 8, 0.89 ms (1.40 PFLOP/s); 16 prompts of up to 2047 tokens 237 us
-// (0.77); 64 caches of up to 8191 positions, one token each, 193 us; one cache
-// of 1000 positions 12 us.
+// heads over 8, 0.88-0.92 ms (1.34-1.40 PFLOP/s, the longer under the power
+// limit at 1980 MHz); 16 prompts of up to 2047 tokens 234 us (0.79); 64 caches
+// of up to 8191 positions, one token each, 193-197 us; one cache of 1000
+// positions 12 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -412,6 +413,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
+// Whether a packed pair holds an infinity or a NaN (all exponent bits set).
+__device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool odd_pair(uint32_t w, __half) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
 // Adds 0 to `sum` for two finite values, NaN for an infinity or a NaN.
 __device__ __forceinline__ __nv_bfloat162 taint(uint32_t w, __nv_bfloat162 sum) {
   return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.f), sum);
@@ -729,7 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = lw; i < boxes; i += kCopyWarps) {
                 const int row = __shfl_sync(0xffffffffu, r[0], i);
                 if (issuer)
-                  sv::tma_load_4d(dst + i * a.box / 8 * Sh::kGroup, &map_k, &sh.full[slot], 0, 0, head * (D / 64), row / 8,
+                  sv::tma_load_4d(dst + i * a.box / 8 * Sh::kGroup, &map_k, &sh.full[slot],
+                      0, 0, head * (D / 64), row / 8,
                                   policy);
                 __syncwarp();
               }
@@ -745,7 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int in = i * kAtOnce + sub, spot = 32 * e + in;
                 const int row = __shfl_sync(0xffffffffu, r[e], in & 31);
                 if (i < 32 / kAtOnce)
-                  copy_16(to + Sh::spot(spot, chunk), from + static_cast<unsigned>(max(row, 0)) * entry, row < 0 ? 0 : 16);
+                  copy_16(to + Sh::spot(spot, chunk), from + static_cast<unsigned>(max(row, 0)) * entry,
+                      row < 0 ? 0 : 16);
               }
             }
             copies_arrive(&sh.full[slot]);
@@ -820,7 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t in = (k % 4) * 32;
-            sv::mma_bf16_ss(d, q_desc + (((k / 4) * (kBlock * 128) + in) >> 4), k_desc + (((k / 4) * Sh::kHalf + in) >> 4),
+            sv::mma_bf16_ss(d, q_desc + (((k / 4) * (kBlock * 128) + in) >> 4),
+                k_desc + (((k / 4) * Sh::kHalf + in) >> 4),
                             kIdS, k > 0);
           }
           sv::mma_commit(&sh.s_full[t]);
@@ -1003,14 +1015,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&sh.full[slot], rank / Sh::kStages & 1);
           uint8_t* tile = ring + slot * Sh::kTileBytes;
           const int chunks = D / 8 / parts, c0 = part * chunks;
-          typename Pair<T>::type sum0 = Pair<T>::zero(), sum1 = sum0;
+          // By bits over the cache, by multiplications for prompts.  Over the cache 64 sequences took 193 us
+          // with the bits, 203 with the multiplications (197 unrolled by 8).  Unrolled loops spill in the
+          // prompts' kernel: 16 prompts took 242 us with the bits, 235 with the multiplications.
+          bool odd = false;
+          if constexpr (kPaged) {
+            for (int c = c0; c < c0 + chunks; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(tile + Sh::spot(row, c));
+              odd |= odd_pair(w.x, T()) || odd_pair(w.y, T()) || odd_pair(w.z, T()) || odd_pair(w.w, T());
+            }
+          } else {
+            typename Pair<T>::type sum0 = Pair<T>::zero(), sum1 = sum0;
 #pragma unroll 1
-          for (int c = c0; c < c0 + chunks; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(tile + Sh::spot(row, c));
-            sum0 = taint(w.x, taint(w.y, sum0));
-            sum1 = taint(w.z, taint(w.w, sum1));
+            for (int c = c0; c < c0 + chunks; ++c) {
+              const uint4 w = *reinterpret_cast<const uint4*>(tile + Sh::spot(row, c));
+              sum0 = taint(w.x, taint(w.y, sum0));
+              sum1 = taint(w.z, taint(w.w, sum1));
+            }
+            odd = tainted(sum0) || tainted(sum1);
           }
-          const bool odd = tainted(sum0) || tainted(sum1);
           const unsigned word = __ballot_sync(0xffffffffu, odd);
           if (lane == 0) sh.spoiled[box][part][warp & 3] = word;
           meet(bar, crowd);
@@ -1284,7 +1307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row < rows && d0 == 0) {
           if (!whole) a.part_ml[base_row + row] = make_float2(base2, all);
-          else if (a.lse) a.lse[base_row + row / a.G * a.heads + row % a.G] = none ? -INFINITY : (base2 + log2f(all)) * kLn2;
+          else if (a.lse) a.lse[base_row + row / a.G * a.heads + row % a.G] =
+              none ? -INFINITY : (base2 + log2f(all)) * kLn2;
         }
       }
       sv::tc_fence_before_sync();
