@@ -438,6 +438,26 @@ def test_more_sequences_than_a_block_has_threads():
     c.check()
 
 
+def test_as_many_sequences_as_a_call_takes():
+    """65535 sequences of one key or none: weight 1, so a row is its value, bit for bit."""
+    B = 65535
+    lens = (torch.arange(B) % 3 != 1).int()
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32), lens.cumsum(0).int()]).cuda()
+    n = int(cu[-1])
+    q, v = (torch.randn((n, h, 64), device="cuda").bfloat16() for h in (2, 1))
+    assert torch.equal(sv.spec_prompt_attention(q, v, v, cu), v.expand(n, 2, 64))
+    entry = torch.randn((B, 1, 128), device="cuda").bfloat16()
+    pool = torch.randn((2, 4, 128), device="cuda").bfloat16()
+    table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    qc = torch.randn((B, 1, 2, 64), device="cuda").bfloat16()
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out = torch.full_like(qc, 7.0)
+    sv.spec_kv_attention(qc, pool, table, zero, entry, q_len=lens.cuda(), out=out)
+    want = torch.where(lens.cuda().bool()[:, None, None, None], entry[:, :, None, 64:].expand(B, 1, 2, 64),
+                       torch.full_like(qc, 7.0))
+    assert torch.equal(out, want)
+
+
 # ---------------------------------------------------------------- together
 def test_a_speculative_round_on_the_cache():
     """A prompt's attention and its entries, two continuations that share them, a tree round on either: the rows
