@@ -955,6 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.cuts[cta] = cut;
       }
       if (t == 1 && !both) {
+        // (Prompts: the tile's next wait for a V tile is by parity, so it must not be an item's loads behind.)
+        if (!kPaged) wait(&sh.o_full[0], used[0] & 1);
         loads += 2 * nb;
         ++used[0];
         ++merges;
@@ -1003,8 +1005,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sv::tc_fence_after_sync();
         };
         unsigned spoil[4] = {0, 0, 0, 0};
-        // Prompts look while the scores are on their way.  (The load before V's in the ring was consumed by the block
-        // before.  Over the cache it may be the other tile's next K, which has landed for sure only with the scores.)
+        // Prompts look while the scores are on their way.  (The load before V's in its slot has landed: this tile's last
+        // products or scores needed it, or the last products of an item that it passed over, for which it waited.
+        // Over the cache it may be the other tile's next K, which has landed for sure only with the scores.)
         if (kPaged) scored();
         if (look) {
           // one row of the V tile per thread; where both tiles read it, each half of the row
@@ -1199,8 +1202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - base2);
         all = ex.sum[par][0][row] * f0 + ex.sum[par][1][row] * f1;
       }
-      wait(&sh.o_full[t0], used[t0] & 1);
-      if (joint) wait(&sh.o_full[1], used[1] & 1);
+      wait(&sh.o_full[0], used[0] & 1);  // (by both tiles, item by item, so that neither falls a phase behind)
+      if (joint || t0 == 1) wait(&sh.o_full[1], used[1] & 1);
       sv::tc_fence_after_sync();
       if (alive) {
         const bool none = all == 0.f;

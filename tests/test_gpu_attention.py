@@ -620,3 +620,26 @@ def test_rising_scores(staged):
         k += (torch.arange(600, device="cuda") // 60).to(dtype)[:, None, None]
         out = sv.spec_prompt_attention(q, k, v, cq)
         check_prompts(q, k, v, cq, ck, out, None, dtype, rows=np.arange(0, 600, 7))
+
+
+@pytest.mark.parametrize("D,n", [(128, 400), (64, 1040)])
+def test_hidden_values_after_an_item_with_one_row_tile(D, n):
+    """The last item of a head has one row tile of 16 tokens and more blocks than the ring of K and V tiles holds (4 at
+    128, 9 at 64); the next head's first item has two, and its first block is masked.  One infinite value in the upper
+    half of the columns of an early key reaches the rows that see it and no other."""
+    B, heads, kv_heads, key, column = 12, 32, 8, 40, D - 3
+    q, k, v, cq, _ = prompts([n] * B, [0] * B, heads, kv_heads, D, torch.bfloat16, seed=21)
+    v.view(B, n, kv_heads, D)[:, key, :, column] = float("inf")
+    ws = sv.prompt_attention_workspace(q, k, B)
+    out = sv.spec_prompt_attention(q, k, v, cq, workspace=ws)
+    assert sv.attention_read_error(ws) == 0
+    o = out.view(B, n, heads, D)
+    assert torch.isfinite(o[:, :key]).all() and (o[:, key:, :, column] == float("inf")).all()
+    assert torch.isfinite(o[..., [c for c in range(D) if c != column]]).all()
+    for b in range(B):
+        a = b * n
+        c = torch.tensor([0, key], dtype=torch.int32).cuda()
+        rows = slice(a, a + key)
+        check_prompts(q[rows], k[rows], v[rows], c, c, out[rows], None, torch.bfloat16)
+    for _ in range(5):
+        assert torch.equal(sv.spec_prompt_attention(q, k, v, cq, workspace=ws), out)
