@@ -10,8 +10,10 @@
  *   out_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i),  m_i = max_j s_ij
  *   lse_i = m_i + log sum_j exp(s_ij - m_i)
  * A row that sees no key (or only keys of score -inf) gets out = 0, lse =
- * -inf.  Keys and values that no row may see are never used: not-a-number
- * and infinite values in them have no effect.
+ * -inf.  A row with a score that is not a number gets NaN in out and lse; a
+ * value that is infinite or not a number and seen makes its column of the row
+ * not finite.  Keys and values that no row may see are never used:
+ * not-a-number and infinite values in them have no effect.
  *
  * spec_kv_attention.  S new tokens per sequence (a row of q_len[b] <= S of
  * them where q_len is given; the rows behind are left as they were), L =

@@ -413,6 +413,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
+// x times its part's factor; 0 for a part that is left out (factor -1).
+__device__ __forceinline__ float weighed(float x, float factor) { return factor < 0.f ? 0.f : x * factor; }
+
 // Whether a packed pair holds an infinity or a NaN (all exponent bits set).
 __device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
@@ -1196,11 +1199,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ex.ref[par][t][row] = ref;
         ex.sum[par][t][row] = sum;
         meet(3, 256);
+        // A tile whose sum is 0 saw no key (factor -1: left out).  Every other one counts, whatever it holds: scores that
+        // are not numbers leave the reference at -infinity, and an infinite value may have a weight that underflows.
         const float m0 = ex.ref[par][0][row], m1 = ex.ref[par][1][row];
+        const float sum0 = ex.sum[par][0][row], sum1 = ex.sum[par][1][row];
         base2 = fmaxf(m0, m1);
-        f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - base2);
-        f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - base2);
-        all = ex.sum[par][0][row] * f0 + ex.sum[par][1][row] * f1;
+        f0 = sum0 == 0.f ? -1.f : exp2_approx(m0 - base2);
+        f1 = sum1 == 0.f ? -1.f : exp2_approx(m1 - base2);
+        all = weighed(sum0, f0) + weighed(sum1, f1);
       }
       wait(&sh.o_full[0], used[0] & 1);  // (by both tiles, item by item, so that neither falls a phase behind)
       if (joint || t0 == 1) wait(&sh.o_full[1], used[1] & 1);
@@ -1244,7 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float o2[32];
               sv::tmem_load_32(from + D + d, o2);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+              for (int e = 0; e < 32; ++e) o[e] = weighed(o[e], f0) + weighed(o2[e], f1);
             }
             if (row >= rows) continue;
             if (whole) {
@@ -1276,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sv::tmem_load_16(from + D + d + 16 * h, o2);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                  o[16 * h + e] = (f0 == 0.f ? 0.f : o[16 * h + e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+                  o[16 * h + e] = weighed(o[16 * h + e], f0) + weighed(o2[e], f1);
               }
             }
 #pragma unroll
@@ -1299,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float o2[16];
               sv::tmem_load_16(from + D + d, o2);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o2[e] * f1);
+              for (int e = 0; e < 16; ++e) o[e] = weighed(o[e], f0) + weighed(o2[e], f1);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -1384,7 +1390,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
       for (int q = 0; q < kFew; ++q) ref = fmaxf(ref, ml[q].x);
 #pragma unroll
       for (int q = 0; q < kFew; ++q) {
-        if (ml[q].x == -INFINITY) continue;  // no such piece, or it saw no key
+        if (ml[q].y == 0.f) continue;  // no such piece, or it saw no key (a sum that is not a number counts)
         const float f = exp2_approx(ml[q].x - ref);
         sum += ml[q].y * f;
 #pragma unroll
@@ -1413,13 +1419,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
 #pragma unroll
         for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
         top = fmaxf(top, ref);
-        const float f = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - top);
-        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
+        const float f = ml.y == 0.f ? -1.f : exp2_approx(ml.x - top);
+        const float keep = sum == 0.f ? -1.f : exp2_approx(ref - top);
         ref = top;
-        sum = keep == 0.f ? 0.f : sum * keep;
+        sum = weighed(sum, keep);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = keep == 0.f ? 0.f : o[e] * keep;
-        const float l = f == 0.f ? 0.f : ml.y * f;
+        for (int e = 0; e < kE; ++e) o[e] = weighed(o[e], keep);
+        const float l = weighed(ml.y, f);
         const int n = min(32, last - p0 + 1);
         for (int p = 0; p < n; p += kAhead) {
           if (p > 0) fetch(p0 + p);
@@ -1427,7 +1433,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
           for (int q = 0; q < kAhead; ++q) {
             const float w = __shfl_sync(0xffffffffu, f, (p + q) & 31);
             sum += __shfl_sync(0xffffffffu, l, (p + q) & 31);  // (0 behind the last piece)
-            if (w != 0.f) {
+            if (!(w < 0.f)) {  // (none behind the last piece)
 #pragma unroll
               for (int e = 0; e < kE; ++e) o[e] += x[q][e] * w;
             }

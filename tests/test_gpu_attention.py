@@ -643,3 +643,71 @@ def test_hidden_values_after_an_item_with_one_row_tile(D, n):
         check_prompts(q[rows], k[rows], v[rows], c, c, out[rows], None, torch.bfloat16)
     for _ in range(5):
         assert torch.equal(sv.spec_prompt_attention(q, k, v, cq, workspace=ws), out)
+
+
+@pytest.mark.parametrize("staged", [False, True])
+@pytest.mark.parametrize("L,S", [(300, 1), (1000, 1), (1000, 5), (20000, 1), (20000, 5)])
+def test_a_query_that_is_not_a_number_however_its_cache_is_cut(L, S, staged):
+    """The heads that hold a NaN give NaN, with a few pieces to join and with many; the others what they give alone."""
+    c = Cache([L], S, 4, 1, 64, torch.bfloat16, 16, staged, seed=L + S)
+    c.q[0, S - 1, 1, 7] = float("nan")
+    out, lse, err = c.run()
+    assert err == 0
+    assert out[0, S - 1, 1].isnan().all() and lse[0, S - 1, 1].isnan()
+    sure = torch.ones((S, 4), dtype=torch.bool)
+    sure[S - 1, 1] = False
+    want = [x[sure.numpy()] for x in c.want(0)]
+    check(out[0][sure.cuda()], lse[0][sure.cuda()], want, 64, c.dtype, L + S, c.vmax())
+
+
+@pytest.mark.parametrize("L", [1000, 20000])
+def test_keys_that_are_not_numbers_in_a_piece_of_their_own(L):
+    """A staged NaN key is one token's last block; NaN keys may fill whole blocks: neither may drop out."""
+    c = Cache([L], 1, 4, 2, 128, torch.float16, 16, True, seed=L)
+    c.staged[0, 0, 3] = float("nan")                       # a key of the first head, seen by heads 0 and 1
+    out, lse, err = c.run()
+    assert err == 0 and out[0, 0, :2].isnan().all() and lse[0, 0, :2].isnan().all()
+    want = [x[:, 2:] for x in c.want(0)]
+    check(out[0, :, 2:], lse[0, :, 2:], want, 128, c.dtype, L + 1, float(c.pool.abs().max()))
+    for first, n in ((384, 128), (0, 256), (L - 104, 104)):
+        c = Cache([L], 1, 4, 2, 128, torch.float16, 16, False, seed=L)
+        for p in range(first, first + n):
+            c.pool[int(c.table[0, p // 16]), p % 16, 3] = float("nan")
+        out, lse, err = c.run()
+        assert err == 0 and out[0, 0, :2].isnan().all() and lse[0, 0, :2].isnan().all()
+        assert out[0, 0, 2:].isfinite().all() and lse[0, 0, 2:].isfinite().all()
+
+
+def test_a_prompt_row_that_is_not_a_number():
+    q, k, v, cq, ck = prompts([3000, 500], [0, 0], 4, 2, 128, torch.bfloat16, seed=13)
+    rows = [0, 5, 700, 1499, 2999, 3100]
+    q[rows, 2, 1] = float("nan")
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = sv.spec_prompt_attention(q, k, v, cq, out_lse=lse)
+    assert out[rows, 2].isnan().all() and lse[rows, 2].isnan().all()
+    rest = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    rest[rows, 2] = False
+    assert out[rest].isfinite().all() and lse[rest].isfinite().all()
+
+
+@pytest.mark.parametrize("L", [300, 1000, 20000])
+def test_an_infinite_value_of_a_key_far_below_the_others(L):
+    """Its weight is positive by definition, so the result is not finite, whichever piece the key is in."""
+    for p in (0, 130, 290):
+        c = Cache([L], 1, 2, 1, 64, torch.bfloat16, 16, False, seed=L)
+        c.q[:] = 1.0
+        c.pool[..., :64] = 4.0
+        where = (int(c.table[0, p // 16]), p % 16)
+        c.pool[where][:64] = -60.0                          # (512 lower on the scores' scale)
+        c.pool[where][64 + 5] = float("inf")
+        out, lse, err = c.run()
+        assert err == 0 and not out[..., 5].isfinite().any()
+        assert out[..., :5].isfinite().all() and out[..., 6:].isfinite().all() and lse.isfinite().all()
+    c = Cache([L], 1, 2, 1, 64, torch.bfloat16, 16, True, seed=L)   # a staged entry is a block of its own
+    c.q[:] = 1.0
+    c.pool[..., :64] = 4.0
+    c.staged[0, 0, :64] = -60.0
+    c.staged[0, 0, 64 + 5] = float("inf")
+    out, lse, err = c.run()
+    assert err == 0 and not out[..., 5].isfinite().any()
+    assert out[..., :5].isfinite().all() and out[..., 6:].isfinite().all() and lse.isfinite().all()
