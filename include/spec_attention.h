@@ -57,9 +57,10 @@
  *
  * Ownership and asynchrony as in spec_verify.h: caller-owned device memory,
  * work enqueued on `stream`, nothing allocated.  Zero a workspace once before
- * its first use (every call leaves it ready for the next); calls that share
- * one, and captured graphs that do, must not run concurrently.  Equal calls
- * give equal bits.
+ * its first use (every call leaves it ready for the next, of either operator
+ * and of any sizes that it is large enough for); calls that share one, and
+ * captured graphs that do, must not run concurrently.  Equal calls give equal
+ * bits.
  * Alignment: 16 bytes for q, k, v, pool, staged, out and workspace; strides
  * multiples of 8 elements, at least heads*head_dim (kv_heads*head_dim); 4
  * bytes for the rest.  Sizes: head_dim 64 or 128, 1 <= kv_heads, heads a

@@ -1490,16 +1490,17 @@ bool stride_ok(int64_t stride, int heads, int head_dim) {
 }
 
 constexpr int64_t kMaxTokens = 1 << 24;
+constexpr int kMaxBatch = 65535;
 
 bool kv_dims_ok(const spec_kv_attn_dims& d) {
-  return heads_ok(d.heads, d.kv_heads, d.head_dim, d.dtype) && d.B >= 1 && d.B <= 65535 && d.S >= 1 &&
+  return heads_ok(d.heads, d.kv_heads, d.head_dim, d.dtype) && d.B >= 1 && d.B <= kMaxBatch && d.S >= 1 &&
          d.S <= kMaxTree && static_cast<int64_t>(d.B) * d.S <= kMaxTokens && d.page_size >= 1 && d.num_pages >= 1 &&
          d.max_pages >= 1 && static_cast<int64_t>(d.max_pages) * d.page_size < (1ll << 31) &&
          static_cast<int64_t>(d.num_pages) * d.page_size < (1ll << 31) && stride_ok(d.q_stride, d.heads, d.head_dim);
 }
 
 bool prompt_dims_ok(const spec_prompt_dims& d) {
-  return heads_ok(d.heads, d.kv_heads, d.head_dim, d.dtype) && d.B >= 1 && d.B <= 65535 && d.total_q >= 1 &&
+  return heads_ok(d.heads, d.kv_heads, d.head_dim, d.dtype) && d.B >= 1 && d.B <= kMaxBatch && d.total_q >= 1 &&
          d.total_q <= kMaxTokens && d.total_k >= 1 && d.total_k <= kMaxTokens &&
          stride_ok(d.q_stride, d.heads, d.head_dim) && stride_ok(d.k_stride, d.kv_heads, d.head_dim) &&
          stride_ok(d.v_stride, d.kv_heads, d.head_dim);
@@ -1511,11 +1512,14 @@ struct Layout {
   size_t bad, cuts, part_ml, part_o, total;
 };
 
-Layout layout(int B, int head_dim, int tiles) {
+// The control words and the marks, which a call expects to be zero and leaves so, lie in front and take the same bytes
+// for every call: a workspace may serve calls of different batches and of both operators.  What is behind them is
+// written before it is read.
+Layout layout(int head_dim, int tiles) {
   Layout l;
   const size_t rows = static_cast<size_t>(kMaxGrid) * 2 * tiles * kBlock;
   l.bad = sv::kKvCtrlBytes;
-  l.cuts = l.bad + up(4 * static_cast<size_t>(B));
+  l.cuts = l.bad + up(4 * static_cast<size_t>(kMaxBatch));
   l.part_ml = l.cuts + up(sizeof(Cut) * kMaxGrid);
   l.part_o = l.part_ml + up(sizeof(float2) * rows);
   l.total = l.part_o + up(sizeof(float) * rows * head_dim);
@@ -1593,7 +1597,7 @@ spec_status launch(const AttnArgs& a, const CUtensorMap (&maps)[3], const sv::De
 template <bool kPaged>
 spec_status launch(AttnArgs& a, const CUtensorMap (&maps)[3], int head_dim, int dtype, const sv::DeviceInfo& dev,
                    void* workspace, cudaStream_t s) {
-  const Layout l = layout(a.B, head_dim, kTiles<kPaged>);
+  const Layout l = layout(head_dim, kTiles<kPaged>);
   char* ws = static_cast<char*>(workspace);
   a.ctrl = reinterpret_cast<int*>(ws);
   a.bad = reinterpret_cast<int*>(ws + l.bad);
@@ -1611,11 +1615,11 @@ spec_status launch(AttnArgs& a, const CUtensorMap (&maps)[3], int head_dim, int 
 extern "C" {
 
 size_t spec_kv_attention_workspace_bytes(spec_kv_attn_dims dims) {
-  return kv_dims_ok(dims) ? layout(dims.B, dims.head_dim, kTiles<true>).total : 0;
+  return kv_dims_ok(dims) ? layout(dims.head_dim, kTiles<true>).total : 0;
 }
 
 size_t spec_prompt_attention_workspace_bytes(spec_prompt_dims dims) {
-  return prompt_dims_ok(dims) ? layout(dims.B, dims.head_dim, kTiles<false>).total : 0;
+  return prompt_dims_ok(dims) ? layout(dims.head_dim, kTiles<false>).total : 0;
 }
 
 spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* block_table, const int32_t* seq_len,

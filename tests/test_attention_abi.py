@@ -189,3 +189,9 @@ def test_binding_refuses_host_tensors_types_and_shapes(lib):
             fn()
     with pytest.raises(ValueError, match="block_table"):
         sv.spec_kv_release(None, sl, bt[0], ref, 16)
+
+
+def test_an_attention_workspace_does_not_depend_on_the_batch(lib):
+    """One workspace serves calls of any batch: what has to be zero lies at the same place for all."""
+    assert len({lib.spec_kv_attention_workspace_bytes(kv_dims(B=b)) for b in (1, 4, 200, 65535)}) == 1
+    assert len({lib.spec_prompt_attention_workspace_bytes(prompt_dims(B=b)) for b in (1, 4, 200, 65535)}) == 1

@@ -711,3 +711,31 @@ def test_an_infinite_value_of_a_key_far_below_the_others(L):
     out, lse, err = c.run()
     assert err == 0 and not out[..., 5].isfinite().any()
     assert out[..., :5].isfinite().all() and out[..., 6:].isfinite().all() and lse.isfinite().all()
+
+
+def test_one_workspace_for_calls_of_different_batches():
+    """A workspace serves calls of any batch it is large enough for, of either operator, one after the other: what one
+    leaves in it marks no sequence of the next as bad."""
+    few = Cache([40, 300, 17, 1000, 60, 7, 129, 500], 2, 4, 2, 64, torch.bfloat16, 16, False, seed=31)
+    many = Cache([5 + b for b in range(200)], 2, 4, 2, 64, torch.bfloat16, 16, False, seed=32)
+    q, k, v, cq, _ = prompts([300, 40, 129], [0] * 3, 4, 2, 64, torch.bfloat16, seed=33)
+    want_few, want_many, want_prompts = few.run()[0], many.run()[0], sv.spec_prompt_attention(q, k, v, cq)
+    ws = max((sv.kv_attention_workspace(many.q, many.pool), sv.prompt_attention_workspace(q, k, 3),
+              sv.kv_attention_workspace(few.q, few.pool)), key=torch.numel)
+    for _ in range(2):
+        for b in (0, 199, 100):
+            assert torch.equal(few.run(workspace=ws)[0], want_few)
+            assert torch.equal(sv.spec_prompt_attention(q, k, v, cq, workspace=ws), want_prompts)
+            was = int(many.seq_len[b])
+            many.seq_len[b] = -1
+            out, lse, err = many.run(workspace=ws)
+            many.seq_len[b] = was
+            assert err == sv.ATTN_DEVERR_LENGTH
+            good = [i for i in range(200) if i != b]
+            assert not out[b].any() and (lse[b] == -float("inf")).all()
+            assert torch.equal(out[good], want_many[good])
+            few.seq_len[3] = -1
+            out, lse, err = few.run(workspace=ws)
+            few.seq_len[3] = 1000
+            good = [i for i in range(8) if i != 3]
+            assert err == sv.ATTN_DEVERR_LENGTH and not out[3].any() and torch.equal(out[good], want_few[good])
