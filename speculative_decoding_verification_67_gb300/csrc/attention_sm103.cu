@@ -84,6 +84,7 @@ constexpr int kMaxTree = 256;
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;        // log2 of the largest weight before O is rescaled
+constexpr float kFar = 1048576.f;    // |reference| from which weights are of scores less their maximum (see the kernel)
 
 // a / b for non-negative values, in 32 bits where they fit (most do; the
 // 64-bit division takes several hundred clocks).
@@ -982,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      float ref = -INFINITY, sum = 0.f;  // the row's reference in log2, the sum of its weights
-      float top = -INFINITY;             // the same reference as a score
+      float top = -INFINITY, sum = 0.f;  // the row's reference as a score, the sum of its weights
+      float limit = -INFINITY;           // a block's maximum beyond it raises the reference; -infinity without one, or far
 
       for (int i = kPaged ? t : 0; i < nb; i += kPaged ? 2 : 1) {
         const bool first = i < (kPaged ? 2 : 1);
@@ -1102,16 +1103,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // raise the reference where a weight would exceed 2^kSlack
-          const bool raise = blk > top && (top == -INFINITY || (blk - top) * c2 > kSlack);
-          if (__any_sync(0xffffffffu, raise) || spoils) {
+          if (__any_sync(0xffffffffu, blk > limit) || spoils) {
             sv::tmem_arrived_32(x[0]);  // its registers are free from here on
-            const float was = ref;
-            if (raise) {
+            float f = 1.f;
+            if (blk > limit && blk > top) {
+              f = top == -INFINITY ? 0.f : exp2_approx(__fmul_rn(top, c2) - __fmul_rn(blk, c2));
               top = blk;
-              ref = top * c2;
+              limit = fabsf(top * c2) > kFar ? -INFINITY : top + kSlack / c2;
             }
             if (!first) {
-              const float f = raise ? (was == -INFINITY ? 0.f : exp2_approx(was - ref)) : 1.f;
               sum *= f;
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
@@ -1124,8 +1124,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               sv::tmem_wait_st();
             }
+            const bool far = limit == -INFINITY && top != -INFINITY;
+            const float less = far ? top : 0.f;
             if (spoils) {  // rare: values that are infinite or not a number, for the rows that see them
-              const float off2 = ref == -INFINITY ? 0.f : -ref;
               if (first) {
                 if (used[t] > 0) wait(&sh.o_free[t], (used[t] - 1) & 1);
                 sv::tc_fence_after_sync();
@@ -1140,7 +1141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
                 if (!(sw >> (c & 31) & 1u)) continue;
                 const bool mine = seen_word(c >> 5) >> (c & 31) & 1u;
-                const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c), c2, off2));
+                const float off2 = limit == -INFINITY ? 0.f : -(top * c2);
+                const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c) - less, c2, off2));
                 const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
@@ -1155,11 +1157,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-
+            // Far: top * c2 is rounded to a reference up to 2^-24 of it away, an exponent that from 2^27 on takes weights
+            // out of fp16's range and from 2^31 on out of bf16's.  The second pass then finds the scores less top (exact
+            // for scores near it) and subtracts nothing.  Every block of such a row comes here, by its limit: a test
+            // beside the limit's cost long prompts 2 %, this one nothing (888-896 us).
+            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll 1
+              for (int c = 0; c < kBlock; c += 32) {
+                float z[32];
+                sv::tmem_load_32(s_addr + c, z);
+                uint32_t u[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(z[e] - less);
+                sv::tmem_store_32(s_addr + c, u);
+              }
+              sv::tmem_wait_st();
+            }
             sv::tmem_start_32(s_addr, x[0]);
           }
-          const float off = ref == -INFINITY ? 0.f : -ref;
-          const float2 cc = make_float2(c2, c2), oo = make_float2(off, off);
+          const float add = limit == -INFINITY ? 0.f : -(top * c2);  // minus the reference
+          const float2 cc = make_float2(c2, c2), oo = make_float2(add, add);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -1194,7 +1211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // in the cache form with both tiles in use each has half of the rows' columns
       const bool joint = kPaged && both;
       const int t0 = kPaged ? 0 : t, width = joint ? D / 2 : D, d0 = joint ? t * width : 0;
-      float f0 = 1.f, f1 = 0.f, all = sum, base2 = ref;
+      float f0 = 1.f, f1 = 0.f, all = sum;
+      const float ref = top * c2;
+      float base2 = ref;
       if (joint) {
         ex.ref[par][t][row] = ref;
         ex.sum[par][t][row] = sum;

@@ -739,3 +739,54 @@ def test_one_workspace_for_calls_of_different_batches():
             few.seq_len[3] = 1000
             good = [i for i in range(8) if i != 3]
             assert err == sv.ATTN_DEVERR_LENGTH and not out[3].any() and torch.equal(out[good], want_few[good])
+
+
+@pytest.mark.parametrize("dtype,powers", [("fp16", [(7, 8), (11, 12), (14, 14), (15, 15)]),
+                                          ("bf16", [(10, 10), (16, 16), (20, 30), (40, 45)])])
+@pytest.mark.parametrize("scale", [0.3, 0.7])
+def test_scores_beyond_24_bits(dtype, powers, scale):
+    """Scores up to 2^84: the weights are one key's or those of exact ties, wherever the largest score stands, rising
+    and falling, negative, and beside rows of small scores.  (Queries and keys of a few bits, so that products are exact
+    in f32; those with the scale are not: by 2^-8 to 2^7 and more in the exponent of a weight.)  The weights that stay
+    are equal, so a result is off by the rounding of the weights (u) and its own (u), and by the sums' and exponentials'
+    share 2^-17 as above; half a step of 2^-24 for the score with its scale, for the sum with the logarithm and for their
+    product is three for the log-sum-exp."""
+    u = torch.finfo(DTYPES[dtype]).eps / 2
+    g = np.random.default_rng(5)
+    for a, b in powers:
+        for kind in ("one", "ties", "up", "down", "negative"):
+            n = 700
+            m = {"one": np.full(n, 0.25), "ties": np.full(n, 0.25), "up": 0.25 * (1 + np.arange(n) // 200),
+                 "down": 0.25 * (4 - np.arange(n) // 200), "negative": np.full(n, -1.0)}[kind]
+            best = g.integers(0, n)
+            m[best] = 1.0 if kind != "negative" else -0.25
+            if kind == "ties":
+                m[g.integers(0, n)] = 1.0
+            c = Cache([n], 2, 4, 2, 64, DTYPES[dtype], 16, False, seed=a + b)
+            c.q[:] = 0
+            c.q[..., 0] = 1.171875 * 2.0 ** a
+            c.q[:, :, 1] = c.q[:, :, 1] * 2.0 ** -a            # a row of small scores in the same warp
+            flat = [int(c.table[0, p // 16]) * 16 + p % 16 for p in range(n)]
+            keys = c.pool.view(-1, 256)
+            keys[:, :128] = 0
+            col = torch.from_numpy(m * 1.3046875 * 2.0 ** b).to(keys).cuda()
+            keys[torch.tensor(flat).cuda(), 0] = col
+            keys[torch.tensor(flat).cuda(), 64] = col
+            q, k, v, cq, ck = prompts([n], [0], 4, 2, 64, DTYPES[dtype], seed=a)
+            q[:], k[:] = 0, 0
+            q[..., 0], k[:, :, 0] = 1.171875 * 2.0 ** a, col[:, None]
+            q[:, 1] = q[:, 1] * 2.0 ** -a
+            got, lse, err = c.run(scale=scale)
+            assert err == 0
+            lse_p = torch.empty(q.shape[:2], device="cuda")
+            got_p = sv.spec_prompt_attention(q, k, v, cq, scale=scale, out_lse=lse_p)
+            rows = np.array([0, 1, 127, 128, 250, 500, 699])
+            want_p = attention.rows(np64(q)[rows], np64(k), np64(v), attention.chain_mask(n, n)[rows],
+                                    float(np.float32(scale)))
+            for x, y, w in ((got[0], lse[0], c.want(0, scale=float(np.float32(scale)))),
+                            (got_p[rows], lse_p[rows], want_p)):
+                x, y = np64(x), np64(y)
+                assert np.isfinite(x).all() and np.isfinite(y).all(), (a, b, kind)
+                far = np.abs(x - w[0]) - (u * np.abs(w[0]) + (u + 2.0 ** -17) * w[2] + 2.0 ** -25)
+                assert (far <= 0).all(), (a, b, kind, far.max(), np.unravel_index(far.argmax(), far.shape))
+                assert (np.abs(y - w[1]) <= 2.0 ** -16 + 3 * 2.0 ** -24 * np.abs(w[1])).all(), (a, b, kind)
