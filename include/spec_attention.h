@@ -53,7 +53,9 @@
  * fp16 (SPEC_ATTN_FP16).  Scores, maxima, sums and outputs accumulate in
  * f32; the weights exp(s - m) are rounded to the input type for the product
  * with the values (a relative error of at most half a step of the type per
- * weight, the size of the rounding of the result), the result once.
+ * weight, the size of the rounding of the result), the result once.  In fp16
+ * a weight of less than 2^-21 is off by up to 2^-32 instead: n keys add at
+ * most n 2^-32 max|v| to the error of out.
  *
  * Ownership and asynchrony as in spec_verify.h: caller-owned device memory,
  * work enqueued on `stream`, nothing allocated.  Zero a workspace once before

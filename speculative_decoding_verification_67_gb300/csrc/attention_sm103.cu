@@ -13,7 +13,10 @@
 // rescaled, only when a later maximum exceeds it by more than 2^8 in weight.
 // Until then weights up to 2^8 stand in P, which costs no precision and spares
 // reading O back for most blocks.  P is rounded to the input type, because that
-// is what the tensor core multiplies; the sum is of the unrounded weights.
+// is what the tensor core multiplies; the sum is of the unrounded weights.  fp16
+// has few small exponents, so there every weight is taken 2^7 times as large (up
+// to 2^15): those below 2^-21 of the reference's are off by 2^-32 of it, not those
+// below 2^-14 by 2^-25, which many keys beside one large one would add up.
 //
 // Two softmax warpgroups (one row per thread) work on two score tiles, so the
 // tensor core computes for one while the other is in its exponentials:
@@ -475,6 +478,10 @@ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t b_mn) {
   return (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u) | (b_mn << 16) |
          ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+// log2 of what stands in P for a score that equals the reference.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 // The rank of V's load of block i among a segment's loads (cache order K0 K1 V0 K2 V1 ..).
 template <bool kPaged>
@@ -1107,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sv::tmem_arrived_32(x[0]);  // its registers are free from here on
             float f = 1.f;
             if (blk > limit && blk > top) {
-              f = top == -INFINITY ? 0.f : exp2_approx(__fmul_rn(top, c2) - __fmul_rn(blk, c2));
+              f = top == -INFINITY ? 0.f : exp2_approx(fmaf(top, c2, -kLift<T>) - fmaf(blk, c2, -kLift<T>));
               top = blk;
               limit = fabsf(top * c2) > kFar ? -INFINITY : top + kSlack / c2;
             }
@@ -1141,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const unsigned sw = c < 64 ? (c < 32 ? spoil[0] : spoil[1]) : (c < 96 ? spoil[2] : spoil[3]);
                 if (!(sw >> (c & 31) & 1u)) continue;
                 const bool mine = seen_word(c >> 5) >> (c & 31) & 1u;
-                const float off2 = limit == -INFINITY ? 0.f : -(top * c2);
+                const float off2 = limit == -INFINITY ? kLift<T> : fmaf(-top, c2, kLift<T>);
                 const float p = exp2_approx(fmaf(sv::tmem_load_1(s_addr + c) - less, c2, off2));
                 const T* v = value_row<T, D, kPaged>(a, s, at.b, at.kvh, kPaged && a.staged && fresh, pos0 + c);
 #pragma unroll 1
@@ -1175,7 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             sv::tmem_start_32(s_addr, x[0]);
           }
-          const float add = limit == -INFINITY ? 0.f : -(top * c2);  // minus the reference
+          const float add = limit == -INFINITY ? kLift<T> : fmaf(-top, c2, kLift<T>);  // minus the reference
           const float2 cc = make_float2(c2, c2), oo = make_float2(add, add);
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1212,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool joint = kPaged && both;
       const int t0 = kPaged ? 0 : t, width = joint ? D / 2 : D, d0 = joint ? t * width : 0;
       float f0 = 1.f, f1 = 0.f, all = sum;
-      const float ref = top * c2;
+      const float ref = fmaf(top, c2, -kLift<T>);
       float base2 = ref;
       if (joint) {
         ex.ref[par][t][row] = ref;

@@ -790,3 +790,37 @@ def test_scores_beyond_24_bits(dtype, powers, scale):
                 far = np.abs(x - w[0]) - (u * np.abs(w[0]) + (u + 2.0 ** -17) * w[2] + 2.0 ** -25)
                 assert (far <= 0).all(), (a, b, kind, far.max(), np.unravel_index(far.argmax(), far.shape))
                 assert (np.abs(y - w[1]) <= 2.0 ** -16 + 3 * 2.0 ** -24 * np.abs(w[1])).all(), (a, b, kind)
+
+
+def test_small_fp16_weights_beside_a_large_one():
+    """One key far above thousands of others, whose weights of 1.5e-8 (2^-26) together are 1e-4 of the sum and whose
+    values are 1 where that key's is 0.  Weights relative to the reference are rounded with 2^7 of room (at the reference
+    itself 2^7 stands in fp16, and the row's sum is at least that): one below the normal range is off by at most 2^-25,
+    2^-32 of the sum, instead of 2^-25."""
+    n, B = 8000, 160
+    c = Cache([n], 1, 2, 1, 64, torch.float16, 16, False, seed=41)
+    c.q[:] = 0
+    c.q[..., 0] = 4.5
+    c.pool[..., :64] = 0
+    c.pool[..., 64:] = 1
+    c.pool[int(c.table[0, 0]), 0, 0] = 4.0                 # position 0: score 18, value 0
+    c.pool[int(c.table[0, 0]), 0, 64:] = 0
+    want = c.want(0, scale=1.0)
+    assert 1e-4 < want[0].min() and want[0].max() < 1.4e-4
+    out, lse, err = c.run(scale=1.0)                       # cut into pieces
+    assert err == 0
+    check(out[0], lse[0], want, 64, c.dtype, n + 1, 2.0 ** -7)
+    q, table = c.q.expand(B, 1, 2, 64).contiguous(), c.table.expand(B, -1).contiguous()
+    out = sv.spec_kv_attention(q, c.pool, table, c.seq_len.expand(B).contiguous(), scale=1.0)   # one piece each
+    for b in (0, 77, B - 1):
+        check(out[b], None, want, 64, c.dtype, n + 1, 2.0 ** -7)
+    q, k, v, cq, ck = prompts([2000] * 6, [0] * 6, 16, 4, 64, torch.float16, seed=42)
+    q[:], k[:], v[:] = 0, 0, 1
+    q[..., 0] = 4.5
+    k[::2000, :, 0], v[::2000] = 4.0, 0
+    out = sv.spec_prompt_attention(q, k, v, cq, scale=1.0)
+    for b in (0, 5):
+        rows = [0, 1, 600, 1999]
+        want = attention.rows(np64(q[2000 * b:2000 * b + 2000])[rows], np64(k[2000 * b:2000 * b + 2000]),
+                              np64(v[2000 * b:2000 * b + 2000]), attention.chain_mask(2000, 2000)[rows], 1.0)
+        check(out[2000 * b:2000 * b + 2000][rows], None, want, 64, torch.float16, 2000, 2.0 ** -7)
