@@ -68,7 +68,7 @@
  * bytes for the rest.  Sizes: head_dim 64 or 128, 1 <= kv_heads, heads a
  * multiple of kv_heads with heads / kv_heads <= 64, heads <= 1024, 1 <= B <=
  * 65535, 1 <= S <= 256, B*S <= 2^24, total_q and total_k <= 2^24, the
- * position ranges of spec_kv_commit.h, 0 < scale finite.
+ * position ranges of spec_kv_commit.h, 0 < scale, scale * log2 e finite.
  */
 #ifndef SPEC_ATTENTION_H_
 #define SPEC_ATTENTION_H_

@@ -1511,6 +1511,9 @@ bool heads_ok(int heads, int kv_heads, int head_dim, int dtype) {
          heads % kv_heads == 0 && heads / kv_heads <= 64 && (dtype == SPEC_ATTN_BF16 || dtype == SPEC_ATTN_FP16);
 }
 
+// (The kernel works with scale * log2 e, in f32.)
+bool scale_ok(float scale) { return scale > 0.f && std::isfinite(scale * kLog2e); }
+
 bool stride_ok(int64_t stride, int heads, int head_dim) {
   return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * head_dim && stride <= (1ll << 31);
 }
@@ -1653,7 +1656,7 @@ spec_status spec_kv_attention(const void* q, const void* pool, const int32_t* bl
                               float* out_lse, spec_kv_attn_dims dims, void* workspace, size_t workspace_bytes,
                               spec_stream_t stream) {
   if (!q || !pool || !block_table || !seq_len || !out || !workspace) return SPEC_ERR_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return SPEC_ERR_ARG;
+  if (!scale_ok(scale)) return SPEC_ERR_ARG;
   if (!kv_dims_ok(dims)) return SPEC_ERR_DIMS;
   if (misaligned(q, 16) || misaligned(pool, 16) || misaligned(staged, 16) || misaligned(out, 16) ||
       misaligned(workspace, 16) || misaligned(block_table, 4) || misaligned(seq_len, 4) || misaligned(parents, 4) ||
@@ -1711,7 +1714,7 @@ spec_status spec_prompt_attention(const void* q, const void* k, const void* v, c
                                   const int32_t* cu_k, float scale, void* out, float* out_lse, spec_prompt_dims dims,
                                   void* workspace, size_t workspace_bytes, spec_stream_t stream) {
   if (!q || !k || !v || !cu_q || !out || !workspace) return SPEC_ERR_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return SPEC_ERR_ARG;
+  if (!scale_ok(scale)) return SPEC_ERR_ARG;
   if (!prompt_dims_ok(dims)) return SPEC_ERR_DIMS;
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16) || misaligned(workspace, 16) ||
       misaligned(cu_q, 4) || misaligned(cu_k, 4) || misaligned(out_lse, 4))

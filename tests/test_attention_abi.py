@@ -195,3 +195,12 @@ def test_an_attention_workspace_does_not_depend_on_the_batch(lib):
     """One workspace serves calls of any batch: what has to be zero lies at the same place for all."""
     assert len({lib.spec_kv_attention_workspace_bytes(kv_dims(B=b)) for b in (1, 4, 200, 65535)}) == 1
     assert len({lib.spec_prompt_attention_workspace_bytes(prompt_dims(B=b)) for b in (1, 4, 200, 65535)}) == 1
+
+
+@pytest.mark.parametrize("scale", [2.36e38, 3.4e38])
+def test_scales_whose_product_with_log2_e_is_infinite(lib, scale):
+    """(0 times it would not be a number: a row of zero scores is the mean of its values.)"""
+    kv, pr = kv_dims(), prompt_dims()
+    assert lib.spec_kv_attention(GOOD, GOOD, GOOD, GOOD, NULL, NULL, NULL, scale, GOOD, NULL, kv, GOOD, 1 << 40,
+                                 NULL) == ARG
+    assert lib.spec_prompt_attention(GOOD, GOOD, GOOD, GOOD, NULL, scale, GOOD, NULL, pr, GOOD, 1 << 40, NULL) == ARG
