@@ -123,10 +123,10 @@ def compact(table, ref, pool):
     for b in range(table.shape[0]):
         for c in range(table.shape[1]):
             p = int(table[b, c])
-            if p < live:
+            if p < 0:
                 continue
-            if p in to:
-                table[b, c] = to[p]
+            if p < len(ref) and ref[p] > 0:
+                table[b, c] = to.get(p, p)
             else:
                 errors.add("PAGE")
     for p, q in to.items():

@@ -356,21 +356,20 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(const PagesArg
   sv::griddep_launch_dependents();
   if (threadIdx.x == 0) s_err = 0;
   __syncthreads();
+  // where each page's entries go (cnt serves as the map): to the page itself, or -1 for a free one
   long long mine = 0, sum;
   for (long long p = threadIdx.x; p < a.num_pages; p += kPlanThreads) {
     const int r = a.ref[p];
     mine += r > 0;
+    a.cnt[p] = r > 0 ? static_cast<int>(p) : -1;
     if (r < 0) atomicOr(&s_err, SPEC_KV_DEVERR_REF);
   }
   block_scan(mine, warp_sum, sum);
   const int live = static_cast<int>(sum);
   const int holes = collect_pages(a.ref, 0, live, false, live, a.list, warp_sum);
   collect_pages(a.ref, live, a.num_pages, true, holes, a.olds, warp_sum);
-  // where each page at or behind `live` goes (cnt serves as the map); -1 for a free one
-  for (long long p = static_cast<long long>(live) + threadIdx.x; p < a.num_pages; p += kPlanThreads) a.cnt[p] = -1;
-  __syncthreads();
   for (int k = threadIdx.x; k < holes; k += kPlanThreads) {
-    const int to = a.list[k], from = a.olds[k];
+    const int to = a.list[k], from = a.olds[k];  // (a hole's own place in the map stays -1)
     a.cnt[from] = to;
     a.ref[to] = a.ref[from];
     a.ref[from] = 0;
@@ -378,24 +377,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(const PagesArg
   if (threadIdx.x == 0) {
     a.ctrl[sv::kKvErr] = s_err;
     a.ctrl[sv::kKvCount] = holes;
-    a.off[0] = live;
     if (out_num_live) *out_num_live = live;
   }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) kv_compact_copy_kernel(const PagesArgs a) {
   sv::griddep_wait();
-  const int moves = a.ctrl[sv::kKvCount], live = a.off[0];
+  const int moves = a.ctrl[sv::kKvCount];
   // block-table entries
   const long long cells = static_cast<long long>(a.B) * a.max_pages;
   int bits = 0;
   for (long long c = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x; c < cells;
        c += static_cast<long long>(gridDim.x) * kCopyThreads) {
     const int p = a.bt[c];
-    if (p < live) continue;  // held where it stays, or none
+    if (p < 0) continue;
     const int to = p < a.num_pages ? a.cnt[p] : -1;
-    if (to >= 0) a.bt[c] = to;
-    else bits |= SPEC_KV_DEVERR_PAGE;
+    if (to < 0) bits |= SPEC_KV_DEVERR_PAGE;
+    else if (to != p) a.bt[c] = to;
   }
   if (bits) atomicOr(a.ctrl + sv::kKvErr, bits);
   // contents

@@ -246,3 +246,16 @@ def test_path_commit_refusals():
         assert sv.kv_pages_read_error(ws) == word(errors)
         assert np.array_equal(d_len.cpu().numpy(), want_len)
         assert np.array_equal(d_pool.cpu().numpy(), want_pool)
+
+
+def test_compact_reports_entries_of_free_pages_on_either_side():
+    """An entry that names a free page stays as it is and is reported, whether the page lies behind the live ones or is
+    one of the holes that are filled; entries of live pages, moved or not, are not."""
+    for stray, flagged in ((15, True), (25, True), (1, True), (0, True), (2, True), (3, False), (19, False), (-1, False)):
+        st = State(3, 3, 20, 2, layers=2, width=72, seed=stray + 1)
+        st.ref[[3, 19, 12, 7]] = [2, 2, 1, 1]
+        st.table[0], st.table[1], st.table[2] = [19, 3, -1], [19, 12, 7], [-1, stray, -1]
+        st.upload()
+        assert st.compact() == ({"PAGE"} if flagged else set())
+        if flagged:
+            assert int(st.d_table[2, 1]) == stray

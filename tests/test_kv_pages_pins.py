@@ -110,3 +110,13 @@ def test_attention_oracle_by_hand():
     assert attention.ancestors([-1, 0, 0, 1]).tolist() == [[1, 0, 0, 0], [1, 1, 0, 0], [1, 0, 1, 0], [1, 1, 0, 1]]
     assert attention.chain_mask(2, 4).tolist() == [[1, 1, 1, 0], [1, 1, 1, 1]]
     assert attention.chain_mask(3, 1).tolist() == [[0], [0], [1]]
+
+
+def test_compact_reports_an_entry_of_a_page_that_is_filled():
+    # pages 3 and 4 are live and move to 0 and 1; sequence 1 names page 1, free before and another's afterwards
+    table = np.array([[3, 4], [1, -1]], dtype=np.int32)
+    ref = np.array([0, 0, 0, 1, 1, 0], dtype=np.int32)
+    pool = np.arange(6).reshape(1, 6, 1, 1)
+    assert kv_pages.compact(table, ref, pool) == ({"PAGE"}, 2)
+    assert table.tolist() == [[0, 1], [1, -1]] and ref.tolist() == [1, 1, 0, 0, 0, 0]
+    assert kv_pages.compact(table[:1], ref, pool) == (set(), 2)
