@@ -34,7 +34,8 @@
  * holds no page gets one; a column whose page is shared (count > 1) gets a
  * new page, into which the committed slots of the old one (positions below
  * seq_len[b]) are copied in every layer, and the old page's count drops.  As
- * if the sequences were served in order, the last holder of a page keeps it.
+ * if the sequences, and the columns of each, were served in order, the last
+ * holder of a page keeps it.
  * Pages are handed out by ascending sequence and column.  seq_len does not
  * change.  All or nothing: when the call needs more pages than are free,
  * nothing changes (SPEC_KV_DEVERR_POOL).

@@ -46,8 +46,8 @@ struct PagesArgs {
   // plan arrays of the workspace
   int* off;      // [B] rank of the first page a sequence is given; -1 where it is not served
   int4* jobs;    // [B] (old page, new page, slots to copy, -)
-  int* cnt;      // [num_pages] sequences of the call that write a page
-  int* last;     // [num_pages] the highest of them
+  int* cnt;      // [num_pages] entries of the call's write ranges that name a page
+  long long* last;  // [num_pages] the last of them, sequence (upper half) and column
   int* list;     // [num_pages] pages handed out / holes
   int* olds;     // [num_pages] page replaced by the k-th one handed out, or -1 / pages that move
   // copies
@@ -220,11 +220,13 @@ __device__ int collect_pages(const int* ref, int first, int end, bool live, int 
 }
 
 // ------------------------------------------------------------------ reserve
-// Whether the sequence's entry p in its write range is replaced by a new page.
-__device__ __forceinline__ bool replaced(const PagesArgs& a, int p, int b) {
+__device__ __forceinline__ long long entry_key(int b, int c) { return static_cast<long long>(b) << 32 | c; }
+
+// Whether entry p in column c of the sequence's write range is replaced by a new page.
+__device__ __forceinline__ bool replaced(const PagesArgs& a, int p, int b, int c) {
   if (p < 0) return true;
   const int r = a.ref[p];
-  return r > 1 && !(a.cnt[p] >= r && a.last[p] == b);
+  return r > 1 && !(a.cnt[p] >= r && a.last[p] == entry_key(b, c));
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const PagesArgs a, const int32_t* num_new) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const PagesArg
       const int p = row[c];
       if (p >= 0) {
         atomicAdd(a.cnt + p, 1);
-        atomicMax(a.last + p, b);
+        atomicMax(a.last + p, entry_key(b, c));
       }
     }
   }
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const PagesArg
     if (ok) {
       const int L = a.seq_len[b], c1 = (L + num_new[b] - 1) / a.page_size;
       const int* row = row_of(a, b);
-      for (int c = L / a.page_size; c <= c1; ++c) need += replaced(a, row[c], b);
+      for (int c = L / a.page_size; c <= c1; ++c) need += replaced(a, row[c], b, c);
     }
     const long long at = want + block_scan(need, warp_sum, total);
     if (ok) a.off[b] = static_cast<int>(at < a.num_pages ? at : a.num_pages);  // beyond the pool: refused below
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(const PagesArg
     int* row = row_of(a, b);
     for (int c = c0; c <= c1; ++c) {
       const int p = row[c];
-      if (!replaced(a, p, b)) continue;  // counts of held pages change only after this loop
+      if (!replaced(a, p, b, c)) continue;  // counts of held pages change only after this loop
       const int q = a.list[k];
       a.olds[k++] = p;
       row[c] = q;
@@ -424,7 +426,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t workspace_size(const spec_kv_pages_dims& d) {
   return sv::kKvCtrlBytes + up(4 * static_cast<size_t>(d.B)) + up(16 * static_cast<size_t>(d.B)) +
-         4 * up(4 * static_cast<size_t>(d.num_pages));
+         3 * up(4 * static_cast<size_t>(d.num_pages)) + up(8 * static_cast<size_t>(d.num_pages));
 }
 
 spec_status make_args(PagesArgs& a, int32_t* seq_len, int32_t* bt, int32_t* ref, const spec_kv_pages_dims& d, void* ws,
@@ -447,7 +449,9 @@ spec_status make_args(PagesArgs& a, int32_t* seq_len, int32_t* bt, int32_t* ref,
   p += up(4 * static_cast<size_t>(d.B));
   a.jobs = reinterpret_cast<int4*>(p);
   p += up(16 * static_cast<size_t>(d.B));
-  for (int** q : {&a.cnt, &a.last, &a.list, &a.olds}) {
+  a.last = reinterpret_cast<long long*>(p);
+  p += up(8 * static_cast<size_t>(d.num_pages));
+  for (int** q : {&a.cnt, &a.list, &a.olds}) {
     *q = reinterpret_cast<int*>(p);
     p += up(4 * static_cast<size_t>(d.num_pages));
   }

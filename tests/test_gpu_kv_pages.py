@@ -259,3 +259,26 @@ def test_compact_reports_entries_of_free_pages_on_either_side():
         assert st.compact() == ({"PAGE"} if flagged else set())
         if flagged:
             assert int(st.d_table[2, 1]) == stray
+
+
+def test_reserve_where_a_sequence_holds_a_page_twice():
+    """Columns of one sequence that share a page are told apart like those of two: the last one that is written keeps it."""
+    st = State(3, 4, 20, 4, layers=2, width=72, seed=3)
+    st.table[0, :3], st.ref[5], st.ref[6] = [5, 5, 6], 2, 1
+    st.seq_len[0] = 2
+    st.upload()
+    assert st.reserve([9, 0, 0]) == set()
+    assert st.table[0, :3].tolist() == [0, 5, 6]
+    st = State(3, 4, 20, 4, layers=2, width=72, seed=4)
+    st.table[0, :3], st.table[1, :2], st.table[2, :2] = [5, 5, 5], [5, 7], [7, 7]
+    st.ref[[5, 7]] = [4, 3]
+    st.seq_len[:] = [3, 1, 2]
+    st.upload()
+    assert st.reserve([5, 7, 6]) == set()                # sequence 0 leaves its third column
+    assert st.table.tolist() == [[0, 1, 5, -1], [2, 3, -1, -1], [4, 7, -1, -1]]
+    st = State(2, 6, 20, 2, seed=5)
+    st.table[0, :6], st.table[1, :2] = [3, 9, 3, 9, 9, 3], [9, 9]
+    st.ref[[3, 9]] = [3, 5]
+    st.seq_len[:] = [1, 0]
+    st.upload()
+    assert st.reserve([11, 4]) == set()
