@@ -1109,8 +1109,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx[c / 2 & 3] = fmaxf(mx[c / 2 & 3], fmaxf(__uint_as_float(now[c]), __uint_as_float(now[c + 1])));
           }
           const float blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // raise the reference where a weight would exceed 2^kSlack
-          if (__any_sync(0xffffffffu, blk > limit) || spoils) {
+          // raise the reference where a weight would exceed 2^kSlack (rows that the tile does not have hold what lay in
+          // their place before, and send no warp this way)
+          if (__any_sync(0xffffffffu, blk > limit && row < rows) || spoils) {
             sv::tmem_arrived_32(x[0]);  // its registers are free from here on
             float f = 1.f;
             if (blk > limit && blk > top) {

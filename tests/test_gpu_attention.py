@@ -824,3 +824,22 @@ def test_small_fp16_weights_beside_a_large_one():
         want = attention.rows(np64(q[2000 * b:2000 * b + 2000])[rows], np64(k[2000 * b:2000 * b + 2000]),
                               np64(v[2000 * b:2000 * b + 2000]), attention.chain_mask(2000, 2000)[rows], 1.0)
         check(out[2000 * b:2000 * b + 2000][rows], None, want, 64, torch.float16, 2000, 2.0 ** -7)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 60000.0])
+def test_queries_that_are_not_asked_for(dtype, fill):
+    """Rows behind q_len, and rows of q that no sequence names, may hold anything: the others keep their bits."""
+    for staged in (False, True):
+        c = Cache([700, 40, 300], 9, 6, 2, 64, DTYPES[dtype], 16, staged, seed=51)
+        n = torch.tensor([3, 9, 1], dtype=torch.int32).cuda()
+        want, lse, _ = c.run(q_len=n)
+        for b, k in enumerate(n.tolist()):
+            c.q[b, k:] = fill
+        got, lse2, err = c.run(q_len=n)
+        assert err == 0 and torch.equal(got, want) and torch.equal(lse, lse2)
+    q, k, v, _, _ = prompts([900], [0], 6, 2, 128, DTYPES[dtype], seed=52)
+    cq = torch.tensor([5, 430, 430, 800], dtype=torch.int32).cuda()
+    want = sv.spec_prompt_attention(q, k, v, cq)
+    q[:5], q[800:] = fill, fill
+    assert torch.equal(sv.spec_prompt_attention(q, k, v, cq), want)
