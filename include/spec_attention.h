@@ -34,7 +34,7 @@
  * behind the block table, a page id outside [0, num_pages) at a position
  * that is seen, or a bad parent gets out = 0 and lse = -inf in its rows and
  * sets bits of the error word (SPEC_ATTN_DEVERR_*).  (With a q_len outside
- * [0, S] all S rows.)
+ * [0, S] all S rows; a sequence of q_len 0 is not looked at.)
  *
  * spec_prompt_attention.  B sequences packed behind each other: sequence b's
  * queries are rows cu_q[b] .. cu_q[b+1]-1 of q [total_q][heads][head_dim] and

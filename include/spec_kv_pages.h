@@ -49,7 +49,8 @@
  * length, a length behind what is allowed, a page id >= num_pages, a page
  * missing where committed positions lie, or a held page whose count is below
  * 1 is left untouched, sets a bit of the error word, and the others are
- * served.  In spec_kv_compact an entry that names no live page stays as it is
+ * served.  (spec_kv_release looks at the entries that it gives back.)  In
+ * spec_kv_compact an entry that names no live page stays as it is
  * and sets SPEC_KV_DEVERR_PAGE.  What else a wrong count does is the caller's:
  * counts that disagree with the table make pages look free that are not, and
  * of several sequences that give back a page with fewer counts than holders

@@ -730,8 +730,9 @@ def _kv_attn_plan(q_shape, q_strides, dtype, pool_shape, max_pages):
 
 
 def kv_attention_workspace(q, pool) -> torch.Tensor:
-    """A zeroed workspace for :func:`spec_kv_attention` calls shaped like ``q``
-    and ``pool`` (reusable; each call leaves it ready for the next)."""
+    """A zeroed workspace for :func:`spec_kv_attention` calls on heads like those
+    of ``q`` and ``pool`` and any batch (reusable; each call leaves it ready for
+    the next).  A call without one allocates and zeroes its own, about 21 MB."""
     plan = _kv_attn_plan(q.shape, q.stride(), _attn_dtype(q, pool), pool.shape, 1)
     return _scratch(None, plan[1], _one_device(q, "q", pool))
 
@@ -794,8 +795,10 @@ def _prompt_plan(q_shape, q_strides, k_shape, k_strides, v_shape, v_strides, dty
 
 
 def prompt_attention_workspace(q, k, B: int) -> torch.Tensor:
-    """A zeroed workspace for :func:`spec_prompt_attention` calls on ``B``
-    sequences shaped like ``q`` and ``k`` (reusable)."""
+    """A zeroed workspace for :func:`spec_prompt_attention` calls on heads like
+    those of ``q`` and ``k`` and any number of sequences (reusable; it also serves
+    :func:`spec_kv_attention`).  A call without one allocates and zeroes its own,
+    about 42 MB."""
     plan = _prompt_plan(q.shape, q.stride(), k.shape, k.stride(), k.shape, k.stride(), _attn_dtype(q, k), B)
     return _scratch(None, plan[1], _one_device(q, "q", k))
 

@@ -30,7 +30,7 @@
 // two O.  So a tile's next scores wait for its last P V, and a tile's block takes
 // the products' 1024 clocks and ~500 of their latency after the ~1900 of its
 // softmax; two tiles overlap to ~3200 clocks per two blocks.  That chain
-// bounds long prompts (70-73 % of the measured bf16 rate), HBM the cache form
+// bounds long prompts (69-72 % of the measured bf16 rate), HBM the cache form
 // with a full batch, and start, end and join of the items everything short.
 //
 // One CTA per SM walks an equal share of all items' blocks (plus a constant per
@@ -54,9 +54,9 @@
 // see them, by plain multiplications.
 //
 // Measured (GB300, calls one after the other): one prompt of 12301 tokens, 32
-// heads over 8, 0.88-0.92 ms (1.34-1.40 PFLOP/s, the longer under the power
-// limit at 1980 MHz); 16 prompts of up to 2047 tokens 234 us (0.79); 64 caches
-// of up to 8191 positions, one token each, 193-197 us; one cache of 1000
+// heads over 8, 0.89-0.94 ms (1.33-1.40 PFLOP/s, the longer under the power
+// limit at 1980 MHz); 16 prompts of up to 2047 tokens 237-241 us (0.77); 64
+// caches of up to 8191 positions, one token each, 191-198 us; one cache of 1000
 // positions 12 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -749,9 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = lw; i < boxes; i += kCopyWarps) {
                 const int row = __shfl_sync(0xffffffffu, r[0], i);
                 if (issuer)
-                  sv::tma_load_4d(dst + i * a.box / 8 * Sh::kGroup, &map_k, &sh.full[slot],
-                      0, 0, head * (D / 64), row / 8,
-                                  policy);
+                  sv::tma_load_4d(dst + i * a.box / 8 * Sh::kGroup, &map_k, &sh.full[slot], 0, 0, head * (D / 64),
+                                  row / 8, policy);
                 __syncwarp();
               }
               return;
@@ -843,8 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t in = (k % 4) * 32;
             sv::mma_bf16_ss(d, q_desc + (((k / 4) * (kBlock * 128) + in) >> 4),
-                k_desc + (((k / 4) * Sh::kHalf + in) >> 4),
-                            kIdS, k > 0);
+                            k_desc + (((k / 4) * Sh::kHalf + in) >> 4), kIdS, k > 0);
           }
           sv::mma_commit(&sh.s_full[t]);
         }
@@ -977,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i_tok = tok0 + row / a.G;     // this row's token
       const int committed = kPaged && a.staged ? blocks_of(s.base) : at.n;
       const bool tree = kPaged && a.parents != nullptr;
-      if (tree) {
+      if (tree) {  // (a node's depth in dependent loads: 256 nodes in a line take 37 us where a chain of 256 takes 22)
         if (alive) {
           unsigned* anc = ts.anc[t][row];
 #pragma unroll

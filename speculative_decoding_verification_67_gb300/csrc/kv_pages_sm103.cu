@@ -10,13 +10,15 @@
 //  * reserve plans in one CTA (what each sequence needs, an exclusive scan,
 //    the lowest free pages by ballots over the counts, the new entries) and
 //    copies the shared partial pages with a dependent grid, one warp per 4 KB
-//    piece of (sequence, layer).
+//    piece of (sequence, layer).  A thread walks the columns of a sequence's
+//    range, which suits a round's few positions: room for one prompt of 12301
+//    tokens takes 242 us on pages of 16 and 3.8 ms on pages of one.
 //  * compact plans in one CTA (live count, ordered lists of holes and of
 //    pages to move) and moves pages and entries with a dependent grid.
 //
 // The plans are bound by latency: a handful of dependent passes over L2 by
-// one CTA.  The copies are bound by HBM: every moved byte is read once and
-// written once.
+// one CTA (reserve: for each column of the longest range).  The copies are
+// bound by HBM: every moved byte is read once and written once.
 #include <cstdint>
 
 #include "internal.h"
