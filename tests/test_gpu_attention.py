@@ -843,3 +843,31 @@ def test_queries_that_are_not_asked_for(dtype, fill):
     want = sv.spec_prompt_attention(q, k, v, cq)
     q[:5], q[800:] = fill, fill
     assert torch.equal(sv.spec_prompt_attention(q, k, v, cq), want)
+
+
+@pytest.mark.parametrize("dtype,power", [("bf16", 20), ("bf16", 60), ("fp16", 15)])
+def test_scores_beyond_24_bits_beside_values_that_are_not_finite(dtype, power):
+    """Both slow ways in one block: rows that do not see the values are one key's value, to a rounding of the weight and
+    of the result and 2^-17; rows that see one are not finite in its column only."""
+    u, n, D = torch.finfo(DTYPES[dtype]).eps / 2, 300, 64
+    m = np.where(np.arange(n) % 50 == 7, 0.25 + np.arange(n) / 512, 0.125) * 1.3046875   # a larger key every 50 tokens
+    q, k, v, cq, _ = prompts([n], [0], 4, 2, D, DTYPES[dtype], seed=61)
+    q[:], k[:] = 0, 0
+    q[..., 0], k[:, :, 0] = 1.171875 * 2.0 ** power, torch.from_numpy(m * 2.0 ** power).to(k).cuda()[:, None]
+    c = Cache([0], n - 100, 4, 2, D, DTYPES[dtype], 16, True, seed=62)                   # the same as new tokens
+    c.q[0], c.staged[0, :, :2 * D], c.staged[0, :, 2 * D:] = (
+        x[:n - 100].reshape(n - 100, *s) for x, s in ((q, (4, D)), (k, (-1,)), (v, (-1,))))
+    clean = np64(v).copy()
+    v[150, :, 3], v[290, :, 60] = float("inf"), float("nan")
+    c.staged.view(1, n - 100, 2, 2, D)[0, 150, 1, :, 3] = float("inf")
+    out = np64(sv.spec_prompt_attention(q, k, v, cq, scale=0.7))
+    got, _, err = c.run(scale=0.7)
+    assert err == 0
+    want = attention.rows(np64(q), np64(k), clean, attention.chain_mask(n, n), float(np.float32(0.7)))
+    for x, w in ((out, want), (np64(got[0]), [y[:n - 100] for y in want])):
+        bad = np.zeros(x.shape, bool)
+        bad[150:, :, 3] = True
+        bad[290:, :, 60] = True
+        assert np.array_equal(np.isfinite(x), ~bad)
+        far = np.abs(x - w[0]) - (u * np.abs(w[0]) + (u + 2.0 ** -17) * w[2] + 2.0 ** -25)
+        assert (far[~bad] <= 0).all()
