@@ -101,6 +101,7 @@ constexpr int kMaxGroups = kMaxRows / 8;  // softmax warpgroups (of either kind 
 constexpr int kMaxThreads = 32 * (4 * kMaxGroups + 1 + kLoadWarps);
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLargest = 3.4028235e38f;
 constexpr float kSet = 16.f, kMost = 256.f;   // the largest weight times scale in P where a reference is set, and ever
 // Where values are (nearly) zero the weights alone set the reference: at most 2^88 there and 2^96 ever, of which 2^31 can
 // be added.  Where they are large weights get down to 2^-96.
@@ -1032,8 +1033,10 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
             old2 = st.y;
             old3 = st.z;
             rw.turn[own].y = old == -INFINITY;
+            // A row that has seen nothing but scores of -infinity has no reference yet: they weigh nothing against the least
+            // finite one, and the first other score weighs too much.
             if (key < mine) {
-              rw.st[own].y = top == -INFINITY ? 0.f : top * st.x;
+              rw.st[own].y = top == -INFINITY ? -kLargest : top * st.x;
               rw.st[own].z = top == -INFINITY ? 0.f : fmaf(top, st.x, -(top * st.x));
             }
             rw.top[own] = top;
