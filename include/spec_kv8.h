@@ -62,13 +62,21 @@
  * refused, with out = 0 and lse = -inf in their rows, as in spec_attention.h
  * (SPEC_ATTN_DEVERR_*); q_len as there.
  * Precision: the products of the query with 8-bit keys, and of the weights
- * with 8-bit values, are taken with the 16-bit operand split into three 8-bit
- * parts (a query element to 2^-27 of its row's largest, a weight to 2^-11 of
- * itself or 2^-23 of the row's largest weight times its value's scale); those
- * with staged entries are products of 16-bit operands.  Products, maxima and sums
- * accumulate in f32 and the result is rounded once.  Scales must be 0 or
- * positive normal numbers for positions that are seen; a seen value scale
- * beyond 2^96 makes its rows NaN, and the bound above holds from 2^-84 on.
+ * with 8-bit values, are taken with the 16-bit operand split into 8-bit parts;
+ * those with staged entries are products of 16-bit operands, the weights
+ * rounded to the type of q.  A query element is good to 2^-27 of its row's
+ * largest.  A weight times its value's scale is good to 2^-11 of itself or
+ * 2^-26 of the row's largest (staged entries count with a scale of 1),
+ * whichever is more, so n small ones are off by n 2^-26 of it at most.  Behind
+ * positions whose weights are far above all before them (new tokens that
+ * outweigh the cache, a cached key with nearly all of the weight) that is
+ * counted anew, from the next 128 positions' largest on, as far as 2^-32 of the
+ * row's.  Products, maxima and sums accumulate in f32 and the result is rounded
+ * once.  Scales must be 0 or positive normal numbers for positions that are
+ * seen; a seen value scale beyond 2^96 makes its rows NaN, and the bound above
+ * holds from 2^-84 on.  Staged values of 2^64 and more may overflow.  The
+ * scores of a cached key with an infinite code may be NaN where the definition
+ * has an infinity.
  *
  * Ownership and asynchrony as in spec_verify.h: work is enqueued on `stream`,
  * nothing is allocated.  Workspaces are zeroed once before their first use and

@@ -11,25 +11,34 @@
 // tensor core as they are; nothing is converted.  What has more than 8 bits is
 // split instead: a query row, scaled by a power of two, into three e4m3 parts
 //   q = 2^t (q0 + q1 / 32 + q2 / 1024),  q0 = e4m3(q 2^-t), q1 = e4m3(32 (q 2^-t - q0)), ..
-// and a weight likewise, each part a group of RT columns of S, P and O; the
+// and a weight into four, each part a group of RT columns of S, P and O; the
 // products' f32 sums are put together in registers.  Three parts hold 12 bits
 // of an element, down to 2^-27 of the row's largest: bf16 and fp16 queries are
 // split exactly but for elements below 2^-16 of it.  Weights are rounded to fp16
-// before (11 bits, which the parts then hold exactly: packed arithmetic takes
-// half the instructions of 32-bit differences).  (Rows of the tiles that no part
-// uses hold anything; they make columns that nobody reads.)
+// before (11 bits, as three parts would hold them; packed arithmetic takes half
+// the instructions of 32-bit differences), whose subnormal end the fourth part
+// reaches: weights times scale are off by 2^-25 at most where 2^-11 of them is
+// less.  With three parts that was 2^-20, so that thousands of small weights were
+// lost beside a large one (64 caches took 115.3 us with three, 117.1 with four).
+// (Rows of the tiles that no part uses hold anything; they make columns that
+// nobody reads.)
 //
 // Scales differ from page to page, so from key to key: a softmax thread
 // multiplies its key's scores by the key's scale, and its weights by the
 // value's before they are split.  Weights are w = 2^(s c - m) with a reference m
-// set so that the row's largest w vs (vs the value's scale) is 8 to 16; they may
+// set so that the row's largest w vs (vs the value's scale) is 2 to 4; they may
 // grow to 256 (e4m3 holds 448; the parts then take steps of 32).  While all stay
 // below, m does not move: the warps agree by one barrier that takes the or of
 // "some weight is too large".  Otherwise the row's maxima are exchanged, m is set
-// anew, and the sums and O rescaled.  Sums of the unsplit weights in f32 make
-// the denominator, so what m is cancels.  m is kept in two parts, the rounded
-// product of the largest score with c and the rest, so that scores of any size
-// lose nothing beside it.
+// anew, and the sums and O rescaled (0.6 us).  The block after one whose largest
+// weight was far above all before it (or the first) is looked through for rows
+// whose weights have all become small, and m set lower for them: a row's largest
+// weight may be that of a new entry, or of a cached key whose value is nearly
+// zero, and what counts are the others.  (Done for every block, by an or of the
+// rows' bits, it took 118 us for the 64 caches, 42 for the chains.)  Sums of the
+// unsplit weights in f32 make the denominator, so what m is cancels.  m is kept
+// in two parts, the rounded product of the largest score with c and the rest, so
+// that scores of any size lose nothing beside it.
 //
 // The new tokens' entries are 16-bit and come first: their blocks take 16-bit
 // products (kind::f16) of the unsplit queries and of weights rounded to the type
@@ -102,12 +111,22 @@ constexpr int kMaxThreads = 32 * (4 * kMaxGroups + 1 + kLoadWarps);
 constexpr int kJoinThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLargest = 3.4028235e38f;
-constexpr float kSet = 16.f, kMost = 256.f;   // the largest weight times scale in P where a reference is set, and ever
+// The largest weight times scale in P where a reference is set, and ever.  (Set to 16 weights would be good to 2^-28 of the
+// row's largest instead of 2^-26, but 33 chains of 5 with 7 heads would take 117 us for 111, as it is exceeded more often.)
+constexpr float kSet = 4.f, kMost = 256.f;
 // Where values are (nearly) zero the weights alone set the reference: at most 2^88 there and 2^96 ever, of which 2^31 can
 // be added.  Where they are large weights get down to 2^-96.
 constexpr float kWeightShare = 3.2311743e-27f;  // 2^-88: kMost times its inverse is 2^96
 constexpr float kLogUp = 88.f, kLogDown = 96.f;
-constexpr float kFewBits = 0.0078125f, kGrowth = 64.f;  // 2^-7: weights near the largest keep 11 bits; 2^64 at most
+// New entries come first, and their values' scale is 1; a cached one's is the largest magnitude over 448 or 57344.  Their
+// weights are 16-bit operands, which hold larger ones: references are set so that the first cached block of values of about
+// unit size has its weights near the middle of what P takes.
+constexpr float kSetNew4 = 64.f, kSetNew5 = 8192.f, kMostNew = 32768.f;  // (e4m3, e5m2; fp16 holds 65504)
+// Where references have risen by 2^kRise since that was last done (or have been set at first), the next cached block is
+// looked through: a row none of whose weights times scale is as large as kLeast has its reference set anew as well, so that
+// they are off by 2^-17 of the block's largest at most.  What is in O grows by that, by 2^kGrowth at most altogether (what is
+// smaller still counts for nothing in f32).
+constexpr float kLeast = 0.00390625f, kGrowth = 32.f, kRise = 10.f;
 
 // What a join needs to know of an item that was cut, left by the CTA with its first piece.
 struct Cut {
@@ -210,13 +229,14 @@ struct Shape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kN = (3 * RT + 15) / 16 * 16;    // columns of 8-bit products
   static constexpr int kN16 = (RT + 15) / 16 * 16;      // of 16-bit ones
-  static constexpr uint32_t kTmemUsed = (2 + kTeams) * kN;
+  static constexpr int kNP = 4 * RT;                    // of the weights' parts
+  static constexpr uint32_t kTmemUsed = 2 * kN + kTeams * kNP;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   // A slot of the ring: the codes of a block, groups of eight rows of keys and of values by turns (as one box brings both),
   // or the keys or the values of a block of 16-bit entries.
   static constexpr int kSlotBytes = 2 * kBlock * D;
-  static constexpr int kSlots = D == 64 ? 8 : RT <= 16 ? 6 : RT == 32 ? 5 : 4;
-  static constexpr int kPBytes = kN * kBlock > kN16 * kBlock * 2 ? kN * kBlock : kN16 * kBlock * 2;
+  static constexpr int kSlots = D == 64 ? 8 : RT == 8 ? 6 : RT <= 32 ? 5 : 4;
+  static constexpr int kPBytes = kNP * kBlock > kN16 * kBlock * 2 ? kNP * kBlock : kN16 * kBlock * 2;
   static constexpr int kQBytes = kN * D, kQ16Bytes = kN16 * D * 2;
   static constexpr uint32_t kMode = D == 128 ? 2 : 4;  // rows of codes: 128 or 64 bytes, swizzled as long
   static constexpr uint32_t kGroup = 16 * D;           // bytes from eight rows of keys to the next eight
@@ -245,10 +265,13 @@ struct Sync {
 // Of each row of the item, for each team: what turns a score into a weight.
 template <int RT, int kTeams, int kSlots>
 struct Rows {
-  float4 st[kTeams * RT];           // scale of the score (log2), reference (high, low part), -
+  float4 st[kTeams * RT];           // scale of the score (log2), reference (high, low part), what O has grown by (log2)
   float top[kTeams * RT];           // the reference as an unscaled score
   float ex[2][4][kTeams * RT];      // maxima of scores and of weights by [warp of the group][row]
-  float2 turn[kTeams * RT];         // what the row's sum and its O are multiplied by; whether there was a reference
+  unsigned has[kMaxGroups][4];      // by [warpgroup][warp]
+  float2 turn[kTeams * RT];         // what the row's sum and its O are multiplied by; whether there was a reference, then
+                                    // whether it has risen by kRise
+  float risen[kTeams * RT];         // what the reference has risen by since that was looked at (log2)
   float sum[4][kTeams * RT];
   float done[kTeams * RT];          // at the end: what O is multiplied by
   float unit[RT];                   // what a 16-bit score is multiplied by to be of the same scale
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
     const bool issuer = elect_one();
     uint32_t loads = 0, segs = 0, uses[2] = {0, 0};  // before the segment: loads, and blocks by score tile
     const uint32_t type = a.bf16 ? 1u : 0u, fmt = static_cast<uint32_t>(a.format);
-    const uint32_t id_s = idesc(fmt, 0, Sh::kN, 0), id_o = idesc(fmt, 0, Sh::kN, 1, 1);
+    const uint32_t id_s = idesc(fmt, 0, Sh::kN, 0), id_o = idesc(fmt, 0, Sh::kNP, 1, 1);
     const uint32_t id_s16 = idesc(type, type, Sh::kN16, 0), id_o16 = idesc(type, type, Sh::kN16, 1);
     const uint32_t ring_addr = sv::smem_u32(ring), q_addr = sv::smem_u32(q_tile), q16_addr = sv::smem_u32(q16_tile);
     const uint32_t p_addr = sv::smem_u32(p_tile);
@@ -730,7 +753,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
                                     : __shfl_sync(0xffffffffu, (ring_addr + load % Sh::kSlots * Sh::kSlotBytes) >> 4, 0);
         await(sh, &sh.p_full[buf], (uses[buf] + (i >> 1)) & 1);
         sv::tc_fence_after_sync();
-        const uint32_t d = __shfl_sync(0xffffffffu, tmem + (2 + (Sh::kTeams == 2 ? buf : 0)) * Sh::kN, 0);
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + 2 * Sh::kN + (Sh::kTeams == 2 ? buf : 0) * Sh::kNP, 0);
         const uint32_t p = __shfl_sync(0xffffffffu, (p_addr + buf * Sh::kPBytes) >> 4, 0);
         if (issuer) {
           if (fresh) {  // (steps of 16 keys, as far as there are any)
@@ -769,7 +792,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
     const int key = tid & (kBlock - 1), bar = 1 + group;
     const int own0 = team * RT + wg * RH;                      // this warpgroup's first row among the teams'
     const uint32_t lanes = static_cast<uint32_t>(quad) << 21;  // this warp's 32 TMEM lanes
-    const uint32_t o_addr = tmem + (2 + team) * Sh::kN + wg * RH + lanes;
+    const uint32_t o_addr = tmem + 2 * Sh::kN + team * Sh::kNP + wg * RH + lanes;
     const float c2 = a.scale_log2;
     uint32_t loads = 0, uses[2] = {0, 0};
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -892,7 +915,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < RH; ++i) z[i] = 0;
 #pragma unroll
-        for (int p = 0; p < 3; ++p) sv::tmem_store(o_addr + p * RT, z);
+        for (int p = 0; p < 4; ++p) sv::tmem_store(o_addr + p * RT, z);
         sv::tmem_wait_st();
       }
       sv::fence_proxy_async_smem();
@@ -908,6 +931,8 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
         sum[i] = 0.f;
         if (kHeld) held[kHeld ? i : 0] = rw.st[own0 + i];
       }
+      constexpr uint32_t kSome = 0x100, kLarge = 0x200;
+      bool risen = false;  // a row's reference has, by kRise
 #pragma unroll 1
       for (int i = team; i < nb; i += kTeams) {
         const int j = lo + i;
@@ -1012,10 +1037,24 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < RH; k += 2) largest = max_or_nan(largest, w[k], w[k + 1]);
-        // Too large times the value's scale, or alone: then beyond 2^96.  And a reference that a block of new entries has set
-        // (their values' scale is 1) leaves cached weights of small scales few bits: it is set anew with the first of them.
-        const bool settle = !fresh && i >= kTeams && i - kTeams < tails;
-        if (meet_any(bar, 128, !(largest * (vs + kWeightShare) <= kMost) || (settle && inside && vs < kFewBits))) {
+        // too large times the value's scale, or alone: then beyond 2^96
+        bool set = !(largest * (vs + kWeightShare) <= (fresh ? kMostNew : kMost));
+        const bool check = risen && !fresh;
+        if (check) {  // .. or all too small: the rows of which a warp has found a weight of kLeast, a bit each
+          uint32_t has = set ? kLarge : 0u;
+#pragma unroll
+          for (int k = 0; k < RH; ++k) has |= k >= mine || w[k] * vs >= kLeast ? 1u << k : 0u;
+          if (largest * vs != 0.f) has |= kSome;
+          has = __reduce_or_sync(0xffffffffu, has);
+          if (lane == 0) rw.has[group][quad] = has;
+          meet(bar, 128);
+          has = rw.has[group][0] | rw.has[group][1] | rw.has[group][2] | rw.has[group][3];
+          set = has >= kLarge || (has & kSome && (has & (kSome - 1)) != (1u << RH) - 1);
+        } else {
+          set = meet_any(bar, 128, set);
+        }
+        if (check) risen = false;
+        if (set) {
           // ---- references anew; between the barriers a thread per row does what is the row's
           const int own = own0 + key;
 #pragma unroll
@@ -1054,30 +1093,39 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
             const bool none = rw.turn[own].y != 0.f;
             const float most = fmaxf(fmaxf(rw.ex[1][0][own], rw.ex[1][1][own]), fmaxf(rw.ex[1][2][own], rw.ex[1][3][own]));
             // the factor, a power of two, goes into the reference's low part
-            float low = st.z - (most > 0.f ? static_cast<float>(ilog2(__fdividef(kSet, most))) : kLogUp);
+            const float set = !fresh ? kSet : a.format ? kSetNew5 : kSetNew4;
+            float low = st.z - (most > 0.f ? static_cast<float>(ilog2(__fdividef(set, most))) : kLogUp);
             low = fminf(fmaxf(low, st.z - kLogUp), st.z + kLogDown);
-            // what is in O and in the sum never grows, but for that of new entries
-            if (settle && !none) low = fmaxf(low, (old2 - st.y) + old3 - kGrowth);
-            float turn = none ? 0.f : exp2_approx((old2 - st.y) + (old3 - low));
-            if (turn > 1.f && !settle) {
-              low = (old2 - st.y) + old3;
-              turn = exp2_approx((old2 - st.y) + (old3 - low));
+            float turn = 0.f, grown = 0.f, risen = kRise;
+            if (!none) {
+              const float old = (old2 - st.y) + old3;  // the old reference beside the new high part
+              if (low < old)  // what is in O and in the sum grows for blocks of small weights only
+                low = check && !(most * exp2_approx(st.z - old) >= kLeast) ? fmaxf(low, old - (kGrowth - st.w)) : old;
+              grown = fmaxf(st.w + (old - low), 0.f);
+              risen = rw.risen[own] + (low - old);
+              turn = exp2_approx(old - low);
             }
-            if (key < mine) rw.st[own].z = low;
-            rw.turn[own].x = turn;
+            if (key < mine) {
+              rw.st[own].z = low;
+              rw.st[own].w = grown;
+            }
+            rw.turn[own] = make_float2(turn, key < mine && risen >= kRise);
+            rw.risen[own] = risen >= kRise ? 0.f : fmaxf(risen, 0.f);
           }
           if (i >= kTeams) wait_done(i - kTeams);  // O as it stands takes the new units
           meet(bar, 128);
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
             const float4 st = rw.st[own0 + k];
+            const float2 turn = rw.turn[own0 + k];
             if (kHeld) held[kHeld ? k : 0] = st;
-            sum[k] *= rw.turn[own0 + k].x;
+            sum[k] *= turn.x;
+            risen |= turn.y != 0.f;
             w[k] = exp2_approx(fmaf(x[k], st.x, -st.y) - st.z);
           }
           if (i >= kTeams) {
 #pragma unroll 1
-            for (int g = 0; g < 3; ++g) {
+            for (int g = 0; g < 4; ++g) {
               uint32_t o[RH];
               sv::tmem_start(o_addr + g * RT, o);
               sv::tmem_wait_ld();
@@ -1113,12 +1161,12 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < RH; k += 2) u[k / 2] = __floats2half2_rn(w[k] * vs, w[k + 1] * vs);
 #pragma unroll
-          for (int g = 0; g < 3; ++g) {
+          for (int g = 0; g < 4; ++g) {
             uint32_t code[RH / 2];
 #pragma unroll
             for (int k = 0; k < RH / 2; ++k) {
               code[k] = sv::f8_pair_e4m3(u[k]);
-              if (g < 2) u[k] = __hmul2(__hsub2(u[k], sv::f8_halves_e4m3(code[k])), __float2half2_rn(32.f));
+              if (g < 3) u[k] = __hmul2(__hsub2(u[k], sv::f8_halves_e4m3(code[k])), __float2half2_rn(32.f));
             }
             const int n = g * RT + wg * RH;
             const uint32_t to = p_addr + (n >> 4) * (kBlock * 16) + key * 16 + (n & 15);
@@ -1187,18 +1235,21 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1)
       static_assert(kTeams == 1 || RT * D * 4 <= 2 * Sh::kPBytes, "room for a team's rows");
       float o[RH];
       if (used) {
-        uint32_t o0[RH], o1[RH], o2[RH];
+        uint32_t o0[RH], o1[RH], o2[RH], o3[RH];
         sv::tmem_start(o_addr, o0);
         sv::tmem_start(o_addr + RT, o1);
         sv::tmem_start(o_addr + 2 * RT, o2);
+        sv::tmem_start(o_addr + 3 * RT, o3);
         sv::tmem_wait_ld();
         sv::tmem_use(o0);
         sv::tmem_use(o1);
         sv::tmem_use(o2);
+        sv::tmem_use(o3);
 #pragma unroll
         for (int n = 0; n < RH; ++n) {
           const float f = rw.done[own0 + n];
-          o[n] = fmaf(__uint_as_float(o2[n]), 1.f / 1024, fmaf(__uint_as_float(o1[n]), 1.f / 32, __uint_as_float(o0[n])));
+          o[n] = fmaf(__uint_as_float(o3[n]), 1.f / 32768, __uint_as_float(o2[n]) * (1.f / 1024));
+          o[n] += fmaf(__uint_as_float(o1[n]), 1.f / 32, __uint_as_float(o0[n]));
           o[n] = f < 0.f ? 0.f : o[n] * f;
         }
         if (team == 1 && key < D) {
