@@ -21,8 +21,10 @@
  * of all others (m - 512 for T = 0, where the token alone is kept): their
  * weights underflow to 0 in spec_verify_from_logits and
  * spec_tree_verify_from_logits at the same T, so a round on filtered draft and
- * target rows draws exactly from the filtered target.  (The value is finite;
- * it is rounded to f32, and not below -FLT_MAX.)
+ * target rows draws exactly from the filtered target (for |z| / T up to 2^22,
+ * as far as the verify step's exponents go).  (The value is finite: it is
+ * rounded to f32, away from m where f32 is coarser than the difference, and not
+ * below -FLT_MAX.)
  *
  * Weights are computed to 2^-31 of themselves and summed as integers of 2^-46
  * of the largest (2^-(63 - ceil log2 V) where V exceeds 2^17), so sums do not

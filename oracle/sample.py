@@ -53,5 +53,9 @@ def row(z, u, T: float, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0):
 def filtered(z, kept, T: float):
     """The filtered logits, in f32."""
     z = np.asarray(z, dtype=np.float32)
-    gone = np.float32(max(float(z.max()) - 512.0 * (T if T > 0 else 1.0), -float(np.finfo(np.float32).max)))
+    least, away = float(np.finfo(np.float32).min), 512.0 * (T if T > 0 else 1.0)
+    top = float(z.max())
+    gone = np.float32(max(top - away, least))
+    if top - float(gone) < 0.75 * away and gone > least:  # f32 is too coarse here: rounded away from the largest
+        gone = max(np.nextafter(gone, np.float32(least)), np.float32(least))
     return np.where(kept, z, gone)

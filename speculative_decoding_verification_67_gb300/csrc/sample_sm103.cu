@@ -648,7 +648,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
       }
     }
     if (a.out_logits) {
-      const float gone = fmaxf(most - away, -3.4028235e38f);
+      // (where f32 is too coarse for the difference, the next value below: rounded to the largest itself it would weigh 1)
+      const float near = most - away;
+      const float gone = fmaxf(most - near < 0.75f * away ? __fsub_rd(most, away) : near, -3.4028235e38f);
       float* to = a.out_logits + row * a.out_ld + w.begin;
       const bool wide = (reinterpret_cast<uintptr_t>(to - w.shift) & 15) == 0;  // (256 rows of 128256 338 us without, 314 with)
       w.each4([&](int i, float4 v) {
