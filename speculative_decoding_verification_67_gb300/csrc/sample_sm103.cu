@@ -646,6 +646,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
           }
         }
       }
+      // In place the draw must be through with what it reads from memory before any of it is written.
+      if (a.out_logits == a.z && w.n + w.shift > a.cap) __syncthreads();
     }
     if (a.out_logits) {
       // (where f32 is too coarse for the difference, the next value below: rounded to the largest itself it would weigh 1)

@@ -62,3 +62,19 @@ def test_equals_that_were_removed_through_the_verify_step(T):
     for b in range(B):
         for j in range(int(acc[b]) + 1):
             assert keeps[b * (K + 1) + j, int(tok[b, j])]
+
+
+@pytest.mark.parametrize("T", [1.0, 1e-9, 1e-20])
+@pytest.mark.parametrize("V,R", [(300001, 3), (200000, 300)])
+def test_in_place_beyond_shared_memory(V, R, T):
+    """What a draw reads again from memory is not overwritten before it is through; -FLT_MAX takes the place of nothing."""
+    z, u = rows(R, V, seed=23, sd=1.0)
+    z = (z * 4).round() / 4 + 50
+    z[0] = -torch.finfo(torch.float32).max                    # (equals that no value lies below)
+    for kw in (dict(top_k=1000), dict(top_p=0.37113), dict(min_p=0.9)):
+        want = torch.empty_like(z)
+        tok = sv.spec_sample(z, u, T, out_logits=want, **kw)
+        for _ in range(3):
+            same = z.clone()
+            assert torch.equal(sv.spec_sample(same, u, T, out_logits=same, **kw), tok)
+            assert torch.equal(same, want)
