@@ -38,6 +38,7 @@ import ctypes
 import functools
 import math
 import os
+import warnings
 
 import torch
 
@@ -954,6 +955,12 @@ def spec_kv_fork(src, dst, seq_len, block_table, ref_count, page_size: int, *, w
     return workspace
 
 
+def _scales_stay(pool):
+    if pool.dtype in _F8_FORMATS:
+        warnings.warn("pages of a float8 pool move without their scales: pass scales=, or pool.view(torch.uint8) where the "
+                      "pool has no scale for each page", stacklevel=3)
+
+
 def _page_scales(scales, pool):
     """kv_heads of the scales [layers][num_pages][2][kv_heads] of an 8-bit pool."""
     if scales.dtype != torch.float32 or scales.dim() != 4 or scales.shape[:2] != pool.shape[:2] \
@@ -966,7 +973,10 @@ def spec_kv_reserve(num_new, seq_len, block_table, ref_count, pool, *, scales=No
     """Make the ``num_new`` (int32 [B]) positions behind ``seq_len`` writable:
     new pages where the table holds none, own copies of shared ones.  ``pool``
     [layers, num_pages, page_size, E].  ``scales`` f32 [layers, num_pages, 2,
-    kv_heads] of an 8-bit pool go with their pages.  Returns the workspace."""
+    kv_heads] of an 8-bit pool go with their pages (a float8 pool without them
+    gives a warning).  Returns the workspace."""
+    if scales is None:
+        _scales_stay(pool)
     dev, dims, nbytes = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, seq_len, num_new, pool,
                        workspace, scales)
     layers, entry = _pool_planes(pool, dims.num_pages)
@@ -991,6 +1001,8 @@ def spec_kv_compact(block_table, ref_count, pool, *, scales=None, out_num_live=N
     page_size, E], and their ``scales`` (as in :func:`spec_kv_reserve`) with
     them; ``out_num_live`` int32 [1] receives how many there are.  Returns the
     workspace."""
+    if scales is None:
+        _scales_stay(pool)
     dev, dims, nbytes = _pages(block_table, ref_count, pool.shape[2] if pool.dim() == 4 else 0, None, pool, out_num_live,
                        workspace, scales)
     layers, entry = _pool_planes(pool, dims.num_pages)

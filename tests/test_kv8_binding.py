@@ -1,0 +1,25 @@
+"""What the binding of the 8-bit cache and of sampling says before it looks for a device; runs without a GPU."""
+import warnings
+
+import pytest
+import torch
+
+import speculative_decoding_verification_67_gb300 as sv
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, torch.float8_e5m2])
+def test_pages_of_a_float8_pool_without_scales(dtype):
+    """A warning, as calls with a pool whose scales lie elsewhere go on to work."""
+    pool = torch.zeros((1, 9, 16, 128), dtype=torch.uint8)
+    table, ref, one = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(9, dtype=torch.int32), \
+        torch.zeros(2, dtype=torch.int32)
+    scales = torch.zeros(1, 9, 2, 1)
+    calls = (lambda p, **kw: sv.spec_kv_reserve(one, one, table, ref, p, **kw),
+             lambda p, **kw: sv.spec_kv_compact(table, ref, p, **kw))
+    for call in calls:
+        with pytest.warns(UserWarning, match="scales"), pytest.raises(ValueError, match="CUDA"):
+            call(pool.view(dtype))
+        for args, kw in (((pool,), {}), ((pool.view(dtype),), dict(scales=scales)), ((pool.to(torch.bfloat16),), {})):
+            with warnings.catch_warnings(), pytest.raises(ValueError, match="CUDA"):
+                warnings.simplefilter("error")
+                call(*args, **kw)
