@@ -37,6 +37,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import warnings
 
@@ -1236,6 +1237,11 @@ def _row_floats(t, name, shape):
     return t.shape[1] if t.shape[0] == 1 else t.stride(0)
 
 
+def _count(value):
+    """top_k as the ABI has it: a vocabulary has 2^19 tokens at most, so no count beyond int32 keeps fewer than all."""
+    return max(-0x80000000, min(operator.index(value), 0x7fffffff))
+
+
 def spec_sample(logits, uniforms, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0, out_tokens=None, out_logits=None,
                 workspace=None, stream=None):
     """Draw a token from each row's filtered distribution.
@@ -1262,7 +1268,7 @@ def spec_sample(logits, uniforms, temperature=1.0, *, top_k=0, top_p=1.0, min_p=
             setattr(params, name + "s", value.data_ptr())
             given.append(value)
         else:
-            setattr(params, name, value)
+            setattr(params, name, _count(value) if dtype == torch.int32 else value)
     dev = _one_device(logits, "logits", uniforms, out_tokens, out_logits, workspace, *given)
     if uniforms is not None and (uniforms.dtype != torch.float32 or uniforms.shape != (rows,)
                                  or not uniforms.is_contiguous()):

@@ -23,3 +23,17 @@ def test_pages_of_a_float8_pool_without_scales(dtype):
             with warnings.catch_warnings(), pytest.raises(ValueError, match="CUDA"):
                 warnings.simplefilter("error")
                 call(*args, **kw)
+
+
+@pytest.mark.parametrize("top_k,want", [(0, 0), (7, 7), (-5, -5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                        (2 ** 32 + 5, 2 ** 31 - 1), (-2 ** 40 + 3, -2 ** 31)])
+def test_top_k_beyond_32_bits(monkeypatch, top_k, want):
+    """The setting that reaches the ABI keeps its meaning (2^32 + 5 is not 5)."""
+    seen = []
+    struct = sv.SpecSampleParams
+    monkeypatch.setattr(sv, "SpecSampleParams", lambda *a: seen.append(struct(*a)) or seen[0])
+    with pytest.raises(ValueError, match="CUDA"):
+        sv.spec_sample(torch.zeros(3, 50), torch.zeros(3), top_k=top_k)
+    assert seen[0].top_k == want
+    with pytest.raises(TypeError):
+        sv.spec_sample(torch.zeros(3, 50), torch.zeros(3), top_k=2.0)
