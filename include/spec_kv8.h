@@ -38,8 +38,8 @@
  * A sequence with a negative seq_len, positions behind the block table, a page
  * id outside the pool, or a path that is not strictly ascending within 1 ..
  * S-1 (or as long as S) is left untouched and sets a SPEC_KV_DEVERR_* bit.  Of
- * one call, no two sequences may write the same page (spec_kv8_reserve gives
- * a shared page's writers pages of their own).
+ * one call, no page may be written through two places of the table
+ * (spec_kv8_reserve gives a shared page's writers pages of their own).
  *
  * spec_kv8_reserve, spec_kv8_compact: spec_kv_reserve and spec_kv_compact of
  * spec_kv_pages.h on this pool; the scales of a page that is copied or moved

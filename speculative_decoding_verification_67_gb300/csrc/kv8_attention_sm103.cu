@@ -50,15 +50,17 @@
 // order of the pieces.  Lengths are read on the device only.
 //
 // Bound, where there are many long caches, by HBM: 64 caches of 512 to 8191
-// positions (8 key-value heads of 128, 583 MB) take 114 us, 5.1 TB/s or 75 % of
-// the measured copy; the loads alone take about 100.  The rest is the start and
-// end of each CTA's items (about 5 us each: queries split, the first reference,
-// the 16-bit block, the way out) and the join, 2.5 us.  Short calls are latency:
-// one cache of 1000 positions 15 us, of 120001 54 to 58 (4.2 to 4.5 TB/s), chains
-// of 5 over 8 caches 31 to 33, trees of 40 over 4 caches 26.  Tiles of many rows are
-// bound by the instructions of a weight (a block of 128 keys takes 0.6 us with 8
-// rows, 1.3 with 32, 1.9 with 48), wide trees over short caches by an item's
-// start and end (about 14 us with 48 rows).  What the choices measured (us):
+// positions (8 key-value heads of 128, 583 MB) take 115 to 124 us, 4.7 to 5.1 TB/s
+// or 69 to 75 % of the measured copy; the loads alone take about 100.  The rest is
+// the start and end of each CTA's items (5 to 6 us each: queries split, the first
+// reference, the 16-bit block, the way out) and the join, 2.5 us.  Short calls are
+// latency: one cache of 1000 positions 15 us, of 120001 54 to 58 (4.2 to 4.5 TB/s),
+// chains of 5 over 8 caches 31 to 37 (the more unequal the scores of a head, the
+// more often references are set), trees of 40 over 4 caches 27 to 30.  Tiles of
+// many rows are bound by the instructions of a weight (a block of 128 keys takes
+// 0.75 us with 8 rows, 1.2 with 32, 1.55 with 48), wide trees over short caches by
+// an item's start and end (about 13 us with 48 rows).  What the choices measured
+// when they were made (us):
 //   a box that brings keys and values by turns, not one for each   64 caches 153, 173
 //   128-byte L2 promotion, not 256 (which reads twice from HBM)    120001 positions 58, 66
 //   a warpgroup for eight rows (four of the smallest tile)         chains 44, 84
