@@ -69,14 +69,14 @@
  * 2^-26 of the row's largest (staged entries count with a scale of 1),
  * whichever is more, so n small ones are off by n 2^-26 of it at most.  Behind
  * positions whose weights are far above all before them (new tokens that
- * outweigh the cache, a cached key with nearly all of the weight) that is
- * counted anew, from the next 128 positions' largest on, as far as 2^-32 of the
- * row's.  Products, maxima and sums accumulate in f32 and the result is rounded
- * once.  Scales must be 0 or positive normal numbers for positions that are
- * seen; a seen value scale beyond 2^96 makes its rows NaN, and the bound above
- * holds from 2^-84 on.  Staged values of 2^64 and more may overflow.  The
- * scores of a cached key with an infinite code may be NaN where the definition
- * has an infinity.
+ * outweigh the cache, a cached key with nearly all of the weight) it is good to
+ * 2^-17 of the largest among the next 128 where that is less (but not beyond
+ * 2^-57 of the row's).  Products, maxima and sums accumulate in f32 and the
+ * result is rounded once.  Scales must be 0 or positive normal numbers for
+ * positions that are seen; a seen value scale beyond 2^96 makes its rows NaN (a
+ * key's may), and the bound above holds from 2^-84 on.  Staged values of 2^64
+ * and more may overflow.  The scores of a cached key with an infinite code may
+ * be NaN where the definition has an infinity.
  *
  * Ownership and asynchrony as in spec_verify.h: work is enqueued on `stream`,
  * nothing is allocated.  Workspaces are zeroed once before their first use and
