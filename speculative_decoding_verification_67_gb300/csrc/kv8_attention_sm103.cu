@@ -42,7 +42,8 @@
 //
 // The new tokens' entries are 16-bit and come first: their blocks take 16-bit
 // products (kind::f16) of the unsplit queries and of weights rounded to the type
-// of q, into the first group of columns.
+// of q (both operands of such a product have one type, and no more than the
+// result keeps), into the first group of columns.
 //
 // One CTA per SM walks an equal share of all items' blocks (plus a constant per
 // item).  An item cut between CTAs leaves normalised partial rows with their
